@@ -107,6 +107,32 @@ class HostIO(ctypes.Structure):
     ]
 
 
+class AppendIO(ctypes.Structure):
+    """Mirror of ``fp2_append_io`` (rows, weights and outputs of fp2_append)."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_longlong),
+        ("k_stride", ctypes.c_longlong),
+        ("v_stride", ctypes.c_longlong),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("slot_map", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("rope_scale", ctypes.c_float),
+        ("rotary_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+    ]
+
+
+FP2_DECODE_MAX_Q = 16
+
 _LIB = None
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(Params)
@@ -131,6 +157,12 @@ SIGNATURES = {
     "fp2_mask": (ctypes.c_int, [_VP, ctypes.c_float, ctypes.c_int, _PP]),
     "fp2_attn": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int, ctypes.c_int, _VP,
                                 _PP]),
+    "fp2_page_map": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int, _VP, _VP, _VP, _VP, _VP, _VP,
+                                    _VP, _PP]),
+    "fp2_append": (ctypes.c_int, [ctypes.POINTER(AppendIO), ctypes.c_int, _PP]),
+    "fp2_decode_workspace_size": (ctypes.c_size_t, [_PP]),
+    "fp2_decode": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _VP,
+                                  _PP]),
     "fp2_workspace_init": (ctypes.c_int, [_PP]),
     "fp2_get_status": (ctypes.c_int, [_PP, ctypes.POINTER(ctypes.c_uint32)]),
     "fp2_noalloc_get_status": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint32)]),
@@ -274,6 +306,29 @@ def attn(q, k_cache, v_cache, page_table, cu_seqlens, kept_bits, block: int, dty
                           ctypes.byref(params)), "fp2_attn")
 
 
+def page_map(prefix_lens, new_lens, free_pages, num_free: int, free_head, page_table, cu_seqlens,
+             seqlens_k, positions, slot_map, free_head_out, params: Params) -> None:
+    _check(lib().fp2_page_map(_ptr(prefix_lens), _ptr(new_lens), _ptr(free_pages), num_free,
+                              _ptr(free_head), _ptr(page_table), _ptr(cu_seqlens),
+                              _ptr(seqlens_k), _ptr(positions), _ptr(slot_map),
+                              _ptr(free_head_out), ctypes.byref(params)), "fp2_page_map")
+
+
+def append(io: AppendIO, dtype: int, params: Params) -> None:
+    _check(lib().fp2_append(ctypes.byref(io), dtype, ctypes.byref(params)), "fp2_append")
+
+
+def decode_workspace_size(params: Params) -> int:
+    return int(lib().fp2_decode_workspace_size(ctypes.byref(params)))
+
+
+def decode(q, k_cache, v_cache, page_table, cu_seqlens, block: int, dtype: int, out, lse,
+           params: Params) -> None:
+    _check(lib().fp2_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                            _ptr(cu_seqlens), block, dtype, _ptr(out), _ptr(lse),
+                            ctypes.byref(params)), "fp2_decode")
+
+
 def workspace_init(params: Params) -> None:
     _check(lib().fp2_workspace_init(ctypes.byref(params)), "fp2_workspace_init")
 
@@ -395,3 +450,257 @@ def make_problem(q, k, v, cu_seqlens, *, Hq: int, Hkv: int, d: int, block: int, 
     keep = (seqlens_k, cu_seqlens_k, q_scale, k_scale, v_scale, out_scale, k_block_factor,
             v_block_factor)
     return Problem(q, k, v, page_table, cu_seqlens, out, block, dtype, P, workspace, keep)
+
+
+class _Step:
+    """What the serving-step handles share: the fp2_params, the workspace with
+    the error word, and a call whose arguments are marshalled once.  ``run``
+    queues it on the stream given at construction, or else on torch's current
+    stream of the buffers' device, and returns; ``check`` synchronises that
+    stream and raises on a device-side error."""
+
+    def _setup(self, device, stream, workspace, nbytes: int):
+        import torch
+        self.device = torch.device(device)
+        self._stream = stream
+        self._current = torch.cuda.current_stream
+        self._current_device = torch.cuda.current_device
+        self._guard = torch.cuda.device
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            fresh = True
+        else:
+            fresh = False
+        self.workspace = workspace
+        self.params.workspace = workspace.data_ptr()
+        self.params.workspace_bytes = workspace.numel()
+        if fresh:
+            with self._guard(self.device):
+                self._on_stream()
+                workspace_init(self.params)
+
+    def _on_stream(self):
+        s = self._stream
+        self.params.stream = self._current(self.device).cuda_stream if s is None else s
+
+    def run(self) -> None:
+        if self._current_device() != self.device.index:
+            with self._guard(self.device):
+                return self._launch()
+        return self._launch()
+
+    def _launch(self) -> None:
+        self._on_stream()
+        st = self._fn(*self._args)
+        if st != FP2_OK:
+            raise Fp2Error(st, self._name)
+
+    def check(self) -> None:
+        with self._guard(self.device):
+            self._on_stream()
+            st, det = get_status(self.params)
+        if st != FP2_OK:
+            raise Fp2Error(st, "device", det)
+
+
+def _need(x, name: str, dtypes, device, shape=None, contiguous: bool = True):
+    """Refuses what the C ABI cannot see: a tensor of another device, type,
+    shape or layout than the call will read it as."""
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, not on {device}")
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} has type {x.dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, not {tuple(shape)}")
+    if contiguous and not x.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _storage_types(dtype: int):
+    import torch
+    if dtype == FP2_FP8_E4M3:
+        return (torch.float8_e4m3fn, torch.uint8)
+    return (torch.bfloat16,)
+
+
+class PageMap(_Step):
+    """fp2_page_map on fixed buffers: ``cu_seqlens``, ``seqlens_k``,
+    ``positions``, ``slot_map``, ``page_table`` and ``free_head_out`` hold the
+    step's map after ``run``."""
+
+
+def make_page_map(prefix_lens, new_lens, page_table, free_pages, free_head, *, page_size: int,
+                  num_pages: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
+                  cu_seqlens=None, seqlens_k=None, positions=None, slot_map=None,
+                  free_head_out=None, stream=None, workspace=None) -> PageMap:
+    """Binds fp2_page_map to int32 device tensors; outputs that are not given
+    are allocated with torch.  ``total_q`` is the number of rows of positions
+    and slot_map (>= the step's new tokens; the rest is padding)."""
+    import torch
+    dev, i32 = prefix_lens.device, (torch.int32,)
+    S = int(prefix_lens.numel())
+
+    def new(x, n):
+        return torch.empty(n, dtype=torch.int32, device=dev) if x is None else x
+    m = PageMap()
+    m.prefix_lens, m.new_lens, m.page_table = prefix_lens, new_lens, page_table
+    m.free_pages, m.free_head = free_pages, free_head
+    m.cu_seqlens, m.seqlens_k = new(cu_seqlens, S + 1), new(seqlens_k, S)
+    m.positions, m.slot_map = new(positions, total_q), new(slot_map, total_q)
+    m.free_head_out = new(free_head_out, 1)
+    _need(page_table, "page_table", i32, dev, (S, page_table.shape[-1]))
+    for name, n in (("prefix_lens", S), ("new_lens", S), ("free_pages", free_pages.numel()),
+                    ("free_head", 1), ("cu_seqlens", S + 1), ("seqlens_k", S),
+                    ("positions", total_q), ("slot_map", total_q), ("free_head_out", 1)):
+        _need(getattr(m, name), name, i32, dev, (n,))
+    P = m.params = Params()
+    P.num_seqs, P.total_q = S, int(total_q)
+    P.page_size, P.num_pages = int(page_size), int(num_pages)
+    P.max_pages_per_seq = int(page_table.shape[1])
+    P.max_seqlen_q, P.max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
+    m._setup(dev, stream, workspace, 256)
+    vp = ctypes.c_void_p
+    m._fn, m._name = lib().fp2_page_map, "fp2_page_map"
+    m._args = (vp(_ptr(prefix_lens)), vp(_ptr(new_lens)), vp(_ptr(free_pages)),
+               int(free_pages.numel()), vp(_ptr(free_head)), vp(_ptr(page_table)),
+               vp(_ptr(m.cu_seqlens)), vp(_ptr(m.seqlens_k)), vp(_ptr(m.positions)),
+               vp(_ptr(m.slot_map)), vp(_ptr(m.free_head_out)), ctypes.byref(P))
+    return m
+
+
+class Append(_Step):
+    """fp2_append on fixed buffers: ``q_out`` and the caches hold the step's
+    rows after ``run``."""
+
+
+def make_append(q, k, v, k_cache, v_cache, positions, slot_map, *, dtype: int, inv_freq=None,
+                rotary_dim: int | None = None, interleaved: bool = False, q_weight=None,
+                k_weight=None, eps: float = 1e-6, rope_scale: float = 1.0, q_scale=None,
+                k_scale=None, v_scale=None, q_out=None, stream=None, workspace=None) -> Append:
+    """Binds fp2_append to device tensors.  q [T, Hq, d], k and v [T, Hkv, d]
+    are bf16 and may be slices of one fused row (any token stride); the caches
+    are [num_pages, page_size, Hkv, d] or [total_k, Hkv, d] in the call's
+    dtype; rotary_dim defaults to what inv_freq covers (0 without it)."""
+    import torch
+    dev = q.device
+    T, Hq, d = (int(x) for x in q.shape)
+    Hkv = int(k.shape[1])
+    f32, i32 = (torch.float32,), (torch.int32,)
+    if rotary_dim is None:
+        rotary_dim = 0 if inv_freq is None else 2 * int(inv_freq.numel())
+    kind = _storage_types(dtype)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=kind[0], device=dev)
+    for name, x, h in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        _need(x, name, (torch.bfloat16,), dev, (T, h, d), contiguous=False)
+        if x.stride(2) != 1 or (h > 1 and x.stride(1) != d):
+            raise ValueError(f"{name}: the heads of a token have to be adjacent rows")
+    _need(q_out, "q_out", kind, dev, (T, Hq, d))
+    for name, x in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(x, name, kind, dev, tuple(k_cache.shape[:-2]) + (Hkv, d))
+        if x.dim() not in (3, 4):
+            raise ValueError(f"{name} is neither [rows, Hkv, d] nor [pages, page_size, Hkv, d]")
+    _need(slot_map, "slot_map", i32, dev, (T,))
+    if rotary_dim:
+        _need(positions, "positions", i32, dev, (T,))
+        _need(inv_freq, "inv_freq", f32, dev, (rotary_dim // 2,))
+    for name, x, n in (("q_weight", q_weight, d), ("k_weight", k_weight, d),
+                       ("q_scale", q_scale, Hq), ("k_scale", k_scale, Hkv),
+                       ("v_scale", v_scale, Hkv)):
+        if x is not None:
+            _need(x, name, f32, dev, (n,))
+    a = Append()
+    a.q, a.k, a.v, a.q_out, a.k_cache, a.v_cache = q, k, v, q_out, k_cache, v_cache
+    a._keep = (positions, slot_map, inv_freq, q_weight, k_weight, q_scale, k_scale, v_scale)
+    P, io = Params(), AppendIO()
+    a.params, a.io = P, io
+    P.num_seqs = 1
+    P.num_q_heads, P.num_kv_heads, P.head_dim, P.total_q = Hq, Hkv, d, T
+    if k_cache.dim() == 4:
+        P.num_pages, P.page_size = int(k_cache.shape[0]), int(k_cache.shape[1])
+    else:
+        P.total_k = int(k_cache.shape[0])
+    P.q_scale, P.k_scale, P.v_scale = _ptr(q_scale), _ptr(k_scale), _ptr(v_scale)
+    io.q, io.k, io.v = _ptr(q), _ptr(k), _ptr(v)
+    # (a stride says nothing where there is one row only)
+    io.q_stride, io.k_stride, io.v_stride = ((int(x.stride(0)) if T > 1 else h * d)
+                                             for x, h in ((q, Hq), (k, Hkv), (v, Hkv)))
+    io.q_weight, io.k_weight, io.inv_freq = _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq)
+    io.positions, io.slot_map = _ptr(positions), _ptr(slot_map)
+    io.q_out, io.k_cache, io.v_cache = _ptr(q_out), _ptr(k_cache), _ptr(v_cache)
+    io.eps, io.rope_scale = float(eps), float(rope_scale)
+    io.rotary_dim, io.interleaved = int(rotary_dim), 1 if interleaved else 0
+    a._setup(dev, stream, workspace, 256)
+    a._fn, a._name = lib().fp2_append, "fp2_append"
+    a._args = (ctypes.byref(io), dtype, ctypes.byref(P))
+    return a
+
+
+class Decode(_Step):
+    """fp2_decode on fixed buffers: ``out`` (and ``lse``, or None) hold the
+    attention of the step's tokens after ``run``."""
+
+
+def make_decode(q, k, v, cu_seqlens, *, Hq: int, Hkv: int, d: int, block: int = 128, dtype: int,
+                max_seqlen_q: int, max_seqlen_k: int, seqlens_k=None, cu_seqlens_k=None,
+                page_table=None, page_size: int = 0, q_scale=None, k_scale=None, v_scale=None,
+                out=None, with_lse: bool = False, lse=None, out_dtype: int = FP2_BF16,
+                out_scale=None, k_block_factor=None, v_block_factor=None, stream=None,
+                workspace=None) -> Decode:
+    """Binds fp2_decode to device tensors, with the arguments of make_problem;
+    allocates the workspace and the outputs that are not given."""
+    import torch
+    dev = q.device
+    T, f32, i32 = int(q.shape[0]), (torch.float32,), (torch.int32,)
+    S = int(cu_seqlens.numel() - 1)
+    kind = _storage_types(dtype)
+    _need(q, "q", kind, dev, (T, Hq, d))
+    lead = (int(k.shape[0]), page_size) if page_table is not None else (int(k.shape[0]),)
+    for name, x in (("k", k), ("v", v)):
+        _need(x, name, kind, dev, lead + (Hkv, d))
+    _need(cu_seqlens, "cu_seqlens", i32, dev, (S + 1,))
+    nkb = -(-int(max_seqlen_k) // block)
+    for name, x, types, shape in (
+            ("seqlens_k", seqlens_k, i32, (S,)), ("cu_seqlens_k", cu_seqlens_k, i32, (S + 1,)),
+            ("q_scale", q_scale, f32, (Hq,)), ("k_scale", k_scale, f32, (Hkv,)),
+            ("v_scale", v_scale, f32, (Hkv,)), ("out_scale", out_scale, f32, (Hq,)),
+            ("k_block_factor", k_block_factor, f32, (S, nkb, Hkv)),
+            ("v_block_factor", v_block_factor, f32, (S, nkb, Hkv))):
+        if x is not None:
+            _need(x, name, types, dev, shape)
+    if page_table is not None:
+        _need(page_table, "page_table", i32, dev, (S, page_table.shape[-1]))
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=_storage_types(out_dtype)[0], device=dev)
+    if lse is None and with_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    _need(out, "out", _storage_types(out_dtype), dev, (T, Hq, d))
+    if lse is not None:
+        _need(lse, "lse", f32, dev, (T, Hq))
+    D = Decode()
+    D.q, D.k, D.v, D.out, D.lse = q, k, v, out, lse
+    D.page_table, D.cu_seqlens, D.block, D.dtype = page_table, cu_seqlens, block, dtype
+    D._keep = (seqlens_k, cu_seqlens_k, q_scale, k_scale, v_scale, out_scale, k_block_factor,
+               v_block_factor)
+    P = D.params = Params()
+    P.num_seqs, P.num_q_heads, P.num_kv_heads, P.head_dim = S, Hq, Hkv, d
+    P.total_q = T
+    if page_table is None:
+        P.total_k = int(k.shape[0])
+    else:
+        P.page_size, P.num_pages = int(page_size), int(k.shape[0])
+        P.max_pages_per_seq = int(page_table.shape[1])
+    P.max_seqlen_q, P.max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
+    P.seqlens_k, P.cu_seqlens_k = _ptr(seqlens_k), _ptr(cu_seqlens_k)
+    P.q_scale, P.k_scale, P.v_scale = _ptr(q_scale), _ptr(k_scale), _ptr(v_scale)
+    P.out_dtype, P.out_scale = out_dtype, _ptr(out_scale)
+    P.k_block_factor, P.v_block_factor = _ptr(k_block_factor), _ptr(v_block_factor)
+    nbytes = decode_workspace_size(P)
+    if nbytes == 0:
+        raise Fp2Error(FP2_ERR_INVALID_ARG, "fp2_decode_workspace_size")
+    D._setup(dev, stream, workspace, nbytes)
+    vp = ctypes.c_void_p
+    D._fn, D._name = lib().fp2_decode, "fp2_decode"
+    D._args = (vp(_ptr(q)), vp(_ptr(k)), vp(_ptr(v)), vp(_ptr(page_table)), vp(_ptr(cu_seqlens)),
+               block, dtype, vp(_ptr(out)), vp(_ptr(lse)), ctypes.byref(P))
+    return D

@@ -293,6 +293,119 @@ fp2_status fp2_prefill_host(const fp2_host_io* io, const int32_t* page_table,
                             const int32_t* cu_seqlens, float tau, int block, fp2_dtype dtype,
                             const fp2_params* params);
 
+/* ---------------------------------------------------------------------------
+ * The serving step around the prefill: page map, cache append, decode
+ * ---------------------------------------------------------------------------
+ * A server that prefills with fp2_prefill also has to lay out its pages, write
+ * the new tokens' keys and values, and answer token by token from the same
+ * cache.  These three calls are that step; they share the conventions above
+ * (device pointers, caller-owned buffers, work queued on params->stream,
+ * nothing allocated or synchronised, so all three can be captured into a CUDA
+ * graph) and the error word at the start of params->workspace (here at least
+ * 256 bytes; one workspace may serve all of them when their calls are ordered
+ * on one stream).  The current device must be the one that owns the buffers.
+ */
+
+/* Page table, slot map and lengths of a step, from request lengths that live
+ * on the device.  Sequence b holds prefix_lens[b] tokens (their pages are in
+ * page_table) and gets new_lens[b] more:
+ *   cu_seqlens[b]  = new_lens[0] + ... + new_lens[b-1]        (num_seqs + 1)
+ *   seqlens_k[b]   = prefix_lens[b] + new_lens[b]
+ *   page_table     entries ceil(prefix / page_size) up to
+ *                  ceil(seqlens_k / page_size) of row b are filled from
+ *                  free_pages[*free_head], the next ones in order of b;
+ *                  the other entries stay
+ *   positions[i]   = prefix_lens[b] + i - cu_seqlens[b] for token i of b
+ *   slot_map[i]    = page_table[b][position / page_size] * page_size +
+ *                  position % page_size, its row in the paged cache
+ *   *free_head_out = *free_head + pages taken
+ * Rows cu_seqlens[num_seqs] .. total_q - 1 (a padded batch) get position 0 and
+ * slot -1.  Reads params: num_seqs (1 .. 16384), total_q (rows of positions
+ * and slot_map), page_size (a power of two, 16 .. 256), max_pages_per_seq,
+ * num_pages (num_pages * page_size must fit an int32), max_seqlen_q,
+ * max_seqlen_k, workspace, stream.
+ * The outputs must not overlap the inputs (seqlens_k != prefix_lens,
+ * free_head_out != free_head: keep two and swap them), page_table excepted.
+ * All or nothing: a length outside [0, max_seqlen_q], a prefix below 0 or
+ * seqlens_k above max_seqlen_k (FP2_ERR_INVALID_ARG, detail 1), more new
+ * tokens than total_q (the same), more pages than max_pages_per_seq
+ * (FP2_ERR_DEVICE_BOUNDS, detail 1), or a free list that is too short
+ * (FP2_ERR_DEVICE_BOUNDS, detail 6) is recorded, and the step is empty:
+ * cu_seqlens all 0, seqlens_k = prefix_lens, every slot -1, page_table and
+ * the head unchanged.  A page id outside [0, num_pages) in free_pages or in
+ * the table records FP2_ERR_DEVICE_BOUNDS (detail 3); the new entry and the
+ * slots on that page become -1. */
+fp2_status fp2_page_map(const int32_t* prefix_lens, const int32_t* new_lens,
+                        const int32_t* free_pages, int num_free, const int32_t* free_head,
+                        int32_t* page_table, int32_t* cu_seqlens, int32_t* seqlens_k,
+                        int32_t* positions, int32_t* slot_map, int32_t* free_head_out,
+                        const fp2_params* params);
+
+/* Inputs and outputs of fp2_append (all device pointers). */
+typedef struct fp2_append_io {
+    const void* q;            /* bf16 [total_q] rows of [Hq][d], q_stride elements apart */
+    const void* k;            /* bf16 [total_q] rows of [Hkv][d], k_stride elements apart */
+    const void* v;            /* bf16, v_stride: the three may be slices of one fused row */
+    long long q_stride;       /* multiples of 4 elements, >= the row's width */
+    long long k_stride;
+    long long v_stride;
+    const float* q_weight;    /* [d] weight of the query norm, NULL: no norm of q */
+    const float* k_weight;    /* [d] weight of the key norm, NULL: no norm of k */
+    const float* inv_freq;    /* [rotary_dim / 2] radians per position; NULL if rotary_dim = 0 */
+    const int32_t* positions; /* [total_q]; NULL if rotary_dim = 0 */
+    const int32_t* slot_map;  /* [total_q] row of the cache for each token; -1: not written */
+    void* q_out;              /* [total_q, Hq, d], bf16 or e4m3 as dtype */
+    void* k_cache;            /* the cache of fp2_prefill: [num_pages, page_size, Hkv, d], or */
+    void* v_cache;            /* [total_k, Hkv, d] when params->page_size = 0 */
+    float eps;                /* of the norms, >= 0 */
+    float rope_scale;         /* factor of the rotated pairs (1: a pure rotation) */
+    int rotary_dim;           /* 0 .. d, a multiple of 8: the leading dimensions that rotate */
+    int interleaved;          /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+} fp2_append_io;
+
+/* What stands between a projection and the attention, in one pass: per-head
+ * RMS norm of q and k, the position rotation, and the write of q for the
+ * attention and of k and v into the cache.  For each token and head
+ *   x = x / sqrt(mean(x^2) + eps) * weight                    (q, k)
+ *   (a, b) = rope_scale * (a cos - b sin, b cos + a sin), the angle being
+ *            position * inv_freq[i], taken without rounding it  (q, k)
+ * in fp32, rounded once: to bf16, or (FP2_FP8_E4M3) to e4m3 of x / scale with
+ * params->q_scale, k_scale, v_scale, saturating.  v is only stored.  A slot
+ * outside the cache other than a negative one records FP2_ERR_DEVICE_BOUNDS
+ * (detail 7) and is not written; of two tokens with one slot either may win.
+ * q_out may be q itself when q is bf16 rows without a gap; the other buffers
+ * must not overlap.  Base pointers are 8-byte aligned, outputs 16.
+ * Caches quantised per key block (params->k_block_factor) are not written by
+ * this call: FP2_ERR_UNSUPPORTED.  Reads params: heads, head_dim, total_q,
+ * total_k or page_size and num_pages, scales, workspace, stream. */
+fp2_status fp2_append(const fp2_append_io* io, fp2_dtype dtype, const fp2_params* params);
+
+/* Most new tokens of one sequence in fp2_decode. */
+#define FP2_DECODE_MAX_Q 16
+
+/* Workspace bytes of fp2_decode (0 on invalid params). */
+size_t fp2_decode_workspace_size(const fp2_params* params);
+
+/* Exact causal attention of a few new tokens per sequence (1 when decoding,
+ * up to FP2_DECODE_MAX_Q when drafts are checked, 0 for a sequence that rests)
+ * over the whole cache: query t of sequence b sees keys 0 .. Lk - Lq + t.
+ *   out = sum_j softmax_j(q . k_j / sqrt(d)) v_j,   lse = ln sum_j exp(q . k_j / sqrt(d))
+ * The keys of all sequences and KV heads are cut into equal shares, one per
+ * CTA, whatever the lengths (they are read on the device, so a captured graph
+ * follows them); a head whose keys lie in several shares is joined by a second
+ * kernel.  Arguments, supported shapes and dtypes as fp2_attn (block matters
+ * for k_block_factor and the page size only); out as fp2_prefill's, rows behind
+ * the last sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys
+ * may hold anything, NaN included.  group_masks, attn_kernel and the debug
+ * fields have no effect.  The workspace's contents need not survive between
+ * calls; calls that share one must be ordered on a stream.
+ * max_seqlen_q above FP2_DECODE_MAX_Q: FP2_ERR_UNSUPPORTED (fp2_prefill takes
+ * those).  Device-side errors as fp2_attn; a sequence with bad lengths or a
+ * page id out of range has undefined out and lse rows. */
+fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* page_table, const int32_t* cu_seqlens, int block,
+                      fp2_dtype dtype, void* out, float* lse, const fp2_params* params);
+
 /* Bytes of the library-owned device scratch used by fp2_prefill_noalloc. */
 #define FP2_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)
 
