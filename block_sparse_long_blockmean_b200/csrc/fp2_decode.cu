@@ -2,8 +2,8 @@
 // over the whole KV cache, split over the cache's length and joined.
 //
 // Mathematics: for a packed query row (token x head of a KV group) over keys
-// j, with z_j = q . k_j / sqrt(d) in units of log2: m = max z_j, l = sum
-// 2^(z_j - m), o = sum 2^(z_j - m) v_j, taken in one pass with a running
+// j, with z_j = q . k_j / sqrt(d) in units of log2: m a reference near max z_j,
+// l = sum 2^(z_j - m), o = sum 2^(z_j - m) v_j, taken in one pass with a running
 // (m, l, o).  Two disjoint key ranges join by m = max(m1, m2), l = l1 2^(m1-m)
 // + l2 2^(m2-m), o likewise; out = o / l, lse = ln 2 (m + log2 l).
 //
@@ -13,8 +13,18 @@
 // (sequence, head, tile) that lies in one share is finished there; one that
 // spans several leaves a partial (m, l, o) per share in the workspace and the
 // join kernel reduces them.
+//
+// Products: both on the tensor core with the keys (or the head dimension) as
+// the 16 rows of an m16n8 product and 8 packed query rows as its columns:
+//   S^T (16 keys x 8 rows)  = K (16 x d) Q^T (d x 8)
+//   O^T (d x 8 rows)       += V^T (d x 16 keys) P^T (16 keys x 8 rows)
+// so that a tile of one token and at most 8 group heads wastes nothing, and a
+// lane holds the same two rows of S^T and O^T: the softmax's scaling never
+// crosses lanes.  Decoding reads each K and V byte once for at most 4 tiles of
+// 8 rows; it is bound by the cache's bytes, not by these products.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
+#include <float.h>
 
 #include "fp2_seq.cuh"
 
@@ -22,15 +32,24 @@ namespace fp2 {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kUnit = 16;  // keys of a unit: a unit never crosses a page
-constexpr int R = kDecRows;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kUnit = 16;             // keys of a unit: a unit never crosses a page
+constexpr int kStages = 3;            // of each warp's ring
+constexpr int kStageBytes = 8192;     // K and V rows of one step of a warp
+constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
+constexpr int kCtas = kDecCtas;
+// Weights are taken relative to m = (largest z when m was set) - kLift and may
+// grow to 2^kRoof before m moves: no maximum has to be found in most steps.
+// fp16 weights then span 2^kRoof (its largest is just under 2^16) down to
+// 2^-24, that is 2^-31 of the row's largest.
+constexpr float kLift = 7.f, kRoof = 15.f;
 
 struct Shape {
     long long units;  // of the sequence
     int per_item;     // units of one item: ceil(Lk / kUnit)
     int tiles;        // row tiles per head
 };
+template <int R>
 __device__ __forceinline__ Shape seq_shape(const KParams& p, const SeqInfo& s) {
     Shape x;
     x.per_item = (s.Lk + kUnit - 1) / kUnit;
@@ -38,10 +57,11 @@ __device__ __forceinline__ Shape seq_shape(const KParams& p, const SeqInfo& s) {
     x.units = (long long)x.per_item * x.tiles * p.Hkv;
     return x;
 }
+template <int R>
 __device__ __forceinline__ long long seq_units(const KParams& p, int b) {
     SeqInfo s;
     if (!load_seq(p, b, s) || s.Lq == 0) return 0;
-    return seq_shape(p, s).units;
+    return seq_shape<R>(p, s).units;
 }
 
 // Sum of x over the CTA and the exclusive prefix of the calling thread.
@@ -78,47 +98,100 @@ __device__ __forceinline__ void put_out(const DecodeParams& D, long long row, in
         static_cast<__nv_bfloat16*>(D.out)[at] = __float2bfloat16(x);
     }
 }
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
 
-template <int DH, bool FP8>
-__device__ __forceinline__ void load_row(const void* base, long long row, float* x) {
-    // DH / 32 consecutive values of a row for this lane
-    constexpr int E = DH / 32;
-    const long long at = row * DH + (threadIdx.x & 31) * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if constexpr (FP8) {
-            const uint8_t b = static_cast<const uint8_t*>(base)[at + e];
-            x[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-        } else {
-            x[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at + e]);
-        }
-    }
+// 16 bytes to shared memory, zeros where !on (then nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 -> two fp16, exact.
+__device__ __forceinline__ uint32_t f16_of(uint16_t x) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(d) : "f"(a), "f"(b));
+    return d;
 }
 
-template <int DH, bool FP8>
+// The rows of V^T that product mt of O^T covers: bf16 16 consecutive ones in
+// natural order; e4m3 (two values per 16-bit element of the transposing load)
+// the even ones first.  Column of the head for accumulator pair i (0: rows
+// 0-7 of the product, 1: rows 8-15) of lane group g.
+template <bool FP8>
+__device__ __forceinline__ int out_col(int mt, int i, int g) {
+    return 16 * mt + (FP8 ? 2 * g + i : 8 * i + g);
+}
+
+template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
-    constexpr int E = DH / 32;
-    const KParams& p = D.p;
+    constexpr int R = 8 * NT;                       // packed rows of a tile
+    constexpr int RB = DH * (FP8 ? 1 : 2);          // bytes of a head's row
+    constexpr int CPR = RB / 16;                    // 16-byte chunks of it
+    constexpr int KS = kStageBytes / (2 * kUnit * RB);  // units of a step
+    constexpr int QS = RB / 32;                     // k-steps of the first product
+    constexpr int MT = DH / 16;                     // row blocks of the second
+    constexpr int LROWS = 32 / CPR;                 // rows that a warp copies at once
+    constexpr int OS = DH + 4;                      // row stride of the join in shared memory
+    static_assert(R * OS * 4 <= kStages * kStageBytes, "a warp's partial rows fit its ring");
+    extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ long long sums[kWarps];
     __shared__ int start_seq;
     __shared__ long long start_base;
-    __shared__ float sm_o[kWarps][R][DH];
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
+    const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    const uint32_t my_ring = smem_u32(ring) + warp * kStages * kStageBytes;
 
     // total units, and this CTA's share of them
     long long total = 0;
     for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         long long t;
-        block_prefix(b < p.num_seqs ? seq_units(p, b) : 0, t, sums);
+        block_prefix(b < p.num_seqs ? seq_units<R>(p, b) : 0, t, sums);
         total += t;
     }
-    // a share is at least one unit per warp
-    const long long want = (total + kWarps - 1) / kWarps;
+    // a share is at least one step of each warp
+    const long long want = (total + kWarps * KS - 1) / (kWarps * KS);
     const int ctas = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
     const int c = blockIdx.x;
-    if (threadIdx.x == 0 && c < (int)gridDim.x) D.record[2 * c] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
     if (c >= ctas || total == 0) return;
     auto share = [&](int i) { return total * i / ctas; };
     long long u = share(c);
@@ -129,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
     for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         long long t;
-        const long long n = b < p.num_seqs ? seq_units(p, b) : 0;
+        const long long n = b < p.num_seqs ? seq_units<R>(p, b) : 0;
         const long long at = base + block_prefix(n, t, sums);
         if (n > 0 && at <= u && u < at + n) {
             start_seq = b;
@@ -147,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
             ++b;
             continue;
         }
-        const Shape sh = seq_shape(p, s);
+        const Shape sh = seq_shape<R>(p, s);
         if (u >= seq_at + sh.units) {
             seq_at += sh.units;
             ++b;
@@ -161,96 +234,290 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
 
         // packed rows of the tile: row r is token (tile * R + r) / G, head r % G
         const int rows = min(R, s.Lq * p.G - tile * R);
-        float q[R][E], o[R][E], m[R], l[R];
-        int last[R];  // the row's last visible key
+        const int t_first = tile * R / p.G, t_last = (tile * R + rows - 1) / p.G;
+        const int seen_all = s.P + t_first + 1;  // keys that every row of the tile sees
+        const int seen_any = s.P + t_last + 1;   // keys past it are not read
+
+        // ---- the copies of this warp: steps of KS units, kWarps * KS apart ----
+        const int first = x0 + warp * KS;
+        const int steps = x1 > first ? (x1 - first + kWarps * KS - 1) / (kWarps * KS) : 0;
+        int row_reg = -1;  // lane i: cache row where unit 32 * (n / 32) + i of this warp starts
+        auto unit_at = [&](int n) { return first + (n / KS) * (kWarps * KS) + n % KS; };
+        auto load_rows = [&](int n0) {
+            const int x = unit_at(n0 + lane);
+            row_reg = x < x1 && x * kUnit < seen_any ? (int)key_row(p, s, b, x * kUnit) : -1;
+        };
+        const uint8_t* kbase = static_cast<const uint8_t*>(D.k) + (size_t)hk * RB + (lane % CPR) * 16;
+        const uint8_t* vbase = static_cast<const uint8_t*>(D.v) + (size_t)hk * RB + (lane % CPR) * 16;
+        const long long token = (long long)p.Hkv * RB;  // bytes between two tokens' rows
+        auto issue = [&](int i) {
+            if (i < steps) {
+                const uint32_t dst = my_ring + (i % kStages) * kStageBytes;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = (tile * R + r) / p.G, h = hk * p.G + (tile * R + r) % p.G;
-            last[r] = r < rows ? s.P + t : -1;
-            m[r] = -INFINITY;
-            l[r] = 0.f;
+                for (int kk = 0; kk < KS; ++kk) {
+                    const int n = i * KS + kk;
+                    if ((n & 31) == 0) load_rows(n);
+                    const int row0 = __shfl_sync(~0u, row_reg, n & 31);
+                    const int valid = row0 < 0 ? 0 : min(kUnit, seen_any - unit_at(n) * kUnit);
+                    const long long at = (long long)max(row0, 0) * token;
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[r][e] = o[r][e] = 0.f;
-            if (r < rows) {
-                load_row<DH, FP8>(D.q, (long long)(s.q0 + t) * p.Hq + h, q[r]);
-                const float sc = D.qk_scale * (FP8 ? p.q_scale[h] * p.k_scale[hk] : 1.f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) q[r][e] *= sc;
-            }
-        }
-        for (int x = x0 + warp; x < x1; x += kWarps) {
-            const int j0 = x * kUnit;
-            const long long row0 = key_row(p, s, b, j0);
-            if (row0 < 0) continue;
-            float fk = 1.f, fv = 1.f;
-            if (FP8 && p.kb_fac) {
-                const size_t at = ((size_t)b * p.nkb_max + j0 / p.B) * p.Hkv + hk;
-                fk = p.kb_fac[at];
-                fv = p.vb_fac[at];
-                if (!(fk > 0.f && fk <= 1.f && fv > 0.f && fv <= 1.f)) {
-                    set_error(p.err, kErrInvalid, kDetFactor);
-                    continue;
+                    for (int r0 = 0; r0 < kUnit; r0 += LROWS) {
+                        const int r = r0 + lane / CPR;
+                        const uint32_t to = dst + (kk * kUnit + r) * RB + (((lane % CPR) ^ (r & 7)) << 4);
+                        const bool on = r < valid;
+                        const long long off = on ? at + r * token : 0;
+                        copy16(to, kbase + off, on);
+                        copy16(to + kStageBytes / 2, vbase + off, on);
+                    }
                 }
             }
-            for (int j = j0; j < min(s.Lk, j0 + kUnit); ++j) {
-                float k[E], v[E];
-                load_row<DH, FP8>(D.k, (row0 + j - j0) * p.Hkv + hk, k);
-                load_row<DH, FP8>(D.v, (row0 + j - j0) * p.Hkv + hk, v);
+            copies_commit();
+        };
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (j > last[r]) continue;
-                    float z = 0.f;
+        for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+        // ---- this warp's query columns, running (m, l, o) ----
+        uint32_t qf[NT][QS][2];
+        float sc[NT][2], m[NT][2], l[NT][2], o[NT][MT][4];
+        int last[NT][2];  // last visible key of rows 2 t4, 2 t4 + 1 of the tile
 #pragma unroll
-                    for (int e = 0; e < E; ++e) z += q[r][e] * k[e];
+        for (int nt = 0; nt < NT; ++nt) {
+            const int rq = nt * 8 + g;
+            const int tok = (tile * R + rq) / p.G, h = hk * p.G + (tile * R + rq) % p.G;
+            const uint8_t* q = static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + tok) * p.Hq + h) * RB + 4 * t4;
 #pragma unroll
-                    for (int w = 16; w > 0; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
-                    z *= fk;
-                    const float mn = fmaxf(m[r], z), old = ex2(m[r] - mn), w = ex2(z - mn);
-                    m[r] = mn;
-                    l[r] = l[r] * old + w;
+            for (int ks = 0; ks < QS; ++ks) {
+                qf[nt][ks][0] = rq < rows ? *reinterpret_cast<const uint32_t*>(q + 32 * ks) : 0u;
+                qf[nt][ks][1] = rq < rows ? *reinterpret_cast<const uint32_t*>(q + 32 * ks + 16) : 0u;
+            }
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[r][e] = o[r][e] * old + w * fv * v[e];
+            for (int e = 0; e < 2; ++e) {
+                const int r = min(nt * 8 + 2 * t4 + e, rows - 1);
+                last[nt][e] = s.P + (tile * R + r) / p.G;
+                sc[nt][e] = D.qk_scale;
+                if constexpr (FP8) sc[nt][e] *= p.q_scale[hk * p.G + (tile * R + r) % p.G] * p.k_scale[hk];
+                m[nt][e] = -FLT_MAX;
+                l[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
+        }
+
+        for (int i = 0; i < steps; ++i) {
+            copies_wait<kStages - 2>();
+            __syncwarp();
+            issue(i + kStages - 1);
+            const uint32_t ks0 = my_ring + (i % kStages) * kStageBytes, vs0 = ks0 + kStageBytes / 2;
+            float z[KS][NT][4];
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[kk][nt][e] = 0.f;
+                const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                for (int ks = 0; ks < QS; ++ks) {
+                    uint32_t a[4];
+                    ldsm4(a, ks0 + (kk * kUnit + r) * RB + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (FP8) mma_e4m3(z[kk][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                        else mma_bf16(z[kk][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                    }
+                }
+            }
+            float fv[KS];
+            bool grow = false;
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                const int n = i * KS + kk, x = unit_at(n), j0 = x * kUnit;
+                float fk = 1.f;
+                fv[kk] = 1.f;
+                const bool past = x >= x1;  // beyond the share: another CTA's keys
+                if constexpr (FP8) {
+                    if (p.kb_fac && x < x1) {
+                        const size_t at = ((size_t)b * p.nkb_max + j0 / p.B) * p.Hkv + hk;
+                        fk = p.kb_fac[at];
+                        fv[kk] = p.vb_fac[at];
+                        if (!(fk > 0.f && fk <= 1.f && fv[kk] > 0.f && fv[kk] <= 1.f)) {
+                            set_error(p.err, kErrInvalid, kDetFactor);
+                            fk = fv[kk] = 1.f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y = z[kk][nt][e] * (FP8 ? sc[nt][e & 1] * fk : sc[nt][e & 1]);
+                        if (j0 + kUnit > seen_all || past)
+                            if (past || j0 + g + (e >> 1) * 8 > last[nt][e & 1]) y = -INFINITY;
+                        z[kk][nt][e] = y;
+                        grow |= y - m[nt][e & 1] > kRoof;
+                    }
+            }
+            if (__any_sync(~0u, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = -INFINITY;
+#pragma unroll
+                        for (int kk = 0; kk < KS; ++kk) y = fmaxf(y, fmaxf(z[kk][nt][e], z[kk][nt][e + 2]));
+                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+                        if (y - m[nt][e] > kRoof) {
+                            const float f = ex2(m[nt][e] - (y - kLift));
+                            m[nt][e] = y - kLift;
+                            l[nt][e] *= f;
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                o[nt][mt][e] *= f;
+                                o[nt][mt][e + 2] *= f;
+                            }
+                        }
+                    }
+            }
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                // weights as the 16-bit operand: fp16 (11 bits) beside e4m3 values;
+                // beside bf16 ones two bf16 terms (16 bits), so that the weights'
+                // rounding stays far below the output's
+                uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = ex2(z[kk][nt][e] - m[nt][e & 1]);
+                    l[nt][0] += w[0] + w[2];
+                    l[nt][1] += w[1] + w[3];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if constexpr (FP8) {
+                            hi[nt][e] = transpose8(pack_f16x2(w[2 * e] * fv[kk], w[2 * e + 1] * fv[kk]));
+                        } else {
+                            const uint32_t x = pack_bf16x2(w[2 * e], w[2 * e + 1]);
+                            hi[nt][e] = transpose8(x);
+                            lo[nt][e] = transpose8(pack_bf16x2(w[2 * e] - __uint_as_float(x << 16),
+                                                               w[2 * e + 1] - __uint_as_float(x & 0xFFFF0000u)));
+                        }
+                    }
+                }
+                auto values = [&](int mt, uint32_t (&a)[4]) {  // V^T rows of product mt
+                    if constexpr (FP8) {
+                        // one load covers two products: 16 keys x 32 values
+                        uint32_t v[4];
+                        const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+                        ldsm4_t(v, vs0 + (kk * kUnit + r) * RB + ((((mt & ~1) + (lane >> 4)) ^ (r & 7)) << 4));
+                        const uint32_t x = __byte_perm(v[2 * (mt & 1)], 0, 0x3120), y = __byte_perm(v[2 * (mt & 1) + 1], 0, 0x3120);
+                        a[0] = f16_of((uint16_t)x);
+                        a[1] = f16_of((uint16_t)(x >> 16));
+                        a[2] = f16_of((uint16_t)y);
+                        a[3] = f16_of((uint16_t)(y >> 16));
+                    } else {
+                        const int r = (lane & 7) + (lane >> 4) * 8;
+                        ldsm4_t(a, vs0 + (kk * kUnit + r) * RB + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+                    }
+                };
+                const int j0 = unit_at(i * KS + kk) * kUnit;
+                if (t_first == t_last || j0 + kUnit <= seen_all) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t a[4];
+                        values(mt, a);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (FP8) {
+                                mma_f16(o[nt][mt], a, hi[nt][0], hi[nt][1]);
+                            } else {
+                                mma_bf16(o[nt][mt], a, hi[nt][0], hi[nt][1]);
+                                mma_bf16(o[nt][mt], a, lo[nt][0], lo[nt][1]);
+                            }
+                        }
+                    }
+                } else {
+                    // keys that only the later tokens of the tile see: a weight of 0
+                    // would not keep a value that is not finite out of a product,
+                    // so token by token, from the last, with the rows it does not
+                    // see cleared
+                    for (int tok = t_last; tok >= t_first; --tok) {
+                        const int clear = max(0, s.P + tok + 1 - j0);
+                        for (int y = clear * CPR + lane; y < kUnit * CPR; y += 32)
+                            *reinterpret_cast<uint4*>(ring + (vs0 - smem_u32(ring)) + (kk * kUnit) * RB + y * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        __syncwarp();
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            uint32_t a[4];
+                            values(mt, a);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                if constexpr (FP8) {
+                                    mma_f16(part, a, hi[nt][0], hi[nt][1]);
+                                } else {
+                                    mma_bf16(part, a, hi[nt][0], hi[nt][1]);
+                                    mma_bf16(part, a, lo[nt][0], lo[nt][1]);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (last[nt][e & 1] == s.P + tok) o[nt][mt][e] += part[e];
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
             }
         }
-        // the warps' parts of this segment, joined in shared memory
+        copies_wait<0>();
+        __syncwarp();
+
+        // ---- the warps' parts of this segment, joined in shared memory ----
+        float* mine = reinterpret_cast<float*>(ring + warp * kStages * kStageBytes);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < E; ++e) sm_o[warp][r][lane * E + e] = o[r][e];
-            if (lane == 0) {
-                sm_m[warp][r] = m[r];
-                sm_l[warp][r] = l[r];
+            for (int e = 0; e < 2; ++e) {
+                float y = l[nt][e];
+                y += __shfl_xor_sync(~0u, y, 4);
+                y += __shfl_xor_sync(~0u, y, 8);
+                y += __shfl_xor_sync(~0u, y, 16);
+                const int r = nt * 8 + 2 * t4 + e;
+                if (g == 0) {
+                    sm_m[warp][r] = m[nt][e];
+                    sm_l[warp][r] = y;
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mine[r * OS + out_col<FP8>(mt, 0, g)] = o[nt][mt][e];
+                    mine[r * OS + out_col<FP8>(mt, 1, g)] = o[nt][mt][e + 2];
+                }
             }
-        }
         __syncthreads();
         const bool whole = x0 == 0 && x1 == sh.per_item;
         const int slot = 2 * c + (x0 == 0 ? 1 : 0);
-        for (int r = warp; r < rows; r += kWarps) {
-            float M = -INFINITY, L = 0.f, O[E];
+        for (int y = threadIdx.x; y < rows * DH; y += kThreads) {
+            const int r = y / DH, col = y % DH;
+            float M = -FLT_MAX, L = 0.f, O = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = 0.f;
-#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = sm_m[w][r] == -INFINITY ? 0.f : ex2(sm_m[w][r] - M);
+                const float f = ex2(sm_m[w][r] - M);
                 L += f * sm_l[w][r];
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (f != 0.f) O[e] += f * sm_o[w][r][lane * E + e];
+                O += f * reinterpret_cast<const float*>(ring + w * kStages * kStageBytes)[r * OS + col];
             }
-            const int t = (tile * R + r) / p.G, h = hk * p.G + (tile * R + r) % p.G;
+            const int tok = (tile * R + r) / p.G, h = hk * p.G + (tile * R + r) % p.G;
             if (whole) {
-                const float inv = (FP8 ? p.v_scale[hk] : 1.f) / L;
-#pragma unroll
-                for (int e = 0; e < E; ++e) put_out(D, s.q0 + t, h, lane * E + e, O[e] * inv);
-                if (D.lse && lane == 0)
-                    D.lse[(long long)(s.q0 + t) * p.Hq + h] = (M + log2f(L)) * 0.69314718055994531f;
+                put_out(D, s.q0 + tok, h, col, O * ((FP8 ? p.v_scale[hk] : 1.f) / L));
+                if (D.lse && col == 0) D.lse[(long long)(s.q0 + tok) * p.Hq + h] = lse_of(M, L);
             } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) D.part[((size_t)slot * R + r) * DH + lane * E + e] = O[e];
-                if (lane == 0) {
+                D.part[((size_t)slot * R + r) * DH + col] = O;
+                if (col == 0) {
                     D.part_ml[((size_t)slot * R + r) * 2] = M;
                     D.part_ml[((size_t)slot * R + r) * 2 + 1] = L;
                 }
@@ -271,42 +538,48 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
 
 // grid (shares, R), DH threads: row r of the item that starts in share c and
 // ends in a later one.
-template <int DH, bool FP8>
+template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(DH) join_kernel(DecodeParams D) {
+    constexpr int R = 8 * NT;
     const KParams& p = D.p;
     const int c = blockIdx.x, r = blockIdx.y, col = threadIdx.x;
     const int4 rec = D.record[2 * c];
     if (rec.x == 0) return;
     if (r >= D.record[2 * c + 1].x) return;
     auto slot = [&](int i) { return ((size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R + r); };
-    float M = -INFINITY, L = 0.f, O = 0.f;
+    float M = -FLT_MAX, L = 0.f, O = 0.f;
     for (int i = 0; i < rec.x; ++i) M = fmaxf(M, D.part_ml[2 * slot(i)]);
     for (int i = 0; i < rec.x; ++i) {
-        const float m = D.part_ml[2 * slot(i)];
-        if (m == -INFINITY) continue;
-        const float f = ex2(m - M);
+        const float f = ex2(D.part_ml[2 * slot(i)] - M);
         L += f * D.part_ml[2 * slot(i) + 1];
         O += f * D.part[slot(i) * DH + col];
     }
     const int t = (rec.w * R + r) / p.G, h = rec.z * p.G + (rec.w * R + r) % p.G;
     put_out(D, rec.y + t, h, col, O * ((FP8 ? p.v_scale[rec.z] : 1.f) / L));
-    if (D.lse && col == 0)
-        D.lse[(long long)(rec.y + t) * p.Hq + h] = (M + log2f(L)) * 0.69314718055994531f;
+    if (D.lse && col == 0) D.lse[(long long)(rec.y + t) * p.Hq + h] = lse_of(M, L);
+}
+
+template <int DH, bool FP8, int NT>
+cudaError_t launch(const DecodeParams& D, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<DH, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    decode_kernel<DH, FP8, NT><<<kCtas, kThreads, kSmemBytes, s>>>(D);
+    join_kernel<DH, FP8, NT><<<dim3(kCtas, 8 * NT), DH, 0, s>>>(D);
+    return cudaGetLastError();
 }
 
 template <int DH, bool FP8>
-cudaError_t launch(const DecodeParams& D, cudaStream_t s) {
-    const int ctas = 296;
-    decode_kernel<DH, FP8><<<ctas, kThreads, 0, s>>>(D);
-    join_kernel<DH, FP8><<<dim3(ctas, R), DH, 0, s>>>(D);
-    return cudaGetLastError();
+cudaError_t launch_rows(const DecodeParams& D, cudaStream_t s) {
+    // the smallest tile that holds the rows of the longest sequence, up to 32
+    const int rows = D.p.max_seqlen_q * D.p.G;
+    return rows <= 8 ? launch<DH, FP8, 1>(D, s) : rows <= 16 ? launch<DH, FP8, 2>(D, s) : launch<DH, FP8, 4>(D, s);
 }
 
 }  // namespace
 
 cudaError_t launch_decode(const DecodeParams& D, cudaStream_t s) {
-    if (D.p.d == 128) return D.p.fp8 ? launch<128, true>(D, s) : launch<128, false>(D, s);
-    return launch<64, false>(D, s);
+    if (D.p.d == 128) return D.p.fp8 ? launch_rows<128, true>(D, s) : launch_rows<128, false>(D, s);
+    return launch_rows<64, false>(D, s);
 }
 
 }  // namespace fp2

@@ -104,8 +104,8 @@ struct AppendParams {
 };
 
 // fp2_decode.  p holds what the launch shares with the prefill kernels.
-// Partial results: slot s = rows [kDecRows][d] fp32 in part, (max, sum) pairs
-// [kDecRows][2] in part_ml; CTA c of the split owns slots 2c and 2c + 1.
+// Partial results: slot s = one tile's rows [rows][d] fp32 in part, (reference,
+// sum) pairs [rows][2] in part_ml; CTA c of the split owns slots 2c and 2c + 1.
 struct DecodeParams {
     KParams p;
     const void *q, *k, *v;
@@ -116,8 +116,8 @@ struct DecodeParams {
     int4* record;              // [kDecCtas][2]: what the join kernel has to do
     float qk_scale;            // log2(e) / sqrt(d)
 };
-constexpr int kDecCtas = 592;  // most CTAs of the split: 4 on each of 148 SMs
-constexpr int kDecRows = 8;    // packed query rows (tokens x group heads) of a tile
+constexpr int kDecCtas = 296;  // CTAs of the split: 2 on each of 148 SMs
+constexpr int kDecRows = 32;   // most packed query rows (tokens x group heads) of a tile
 
 cudaError_t launch_page_map(const MapParams& p, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
