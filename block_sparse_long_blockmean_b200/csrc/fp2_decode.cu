@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 #include <float.h>
 
+#include "fp2_launch.cuh"
 #include "fp2_seq.cuh"
 
 namespace fp2 {
@@ -33,11 +34,25 @@ namespace fp2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kUnit = 16;             // keys of a unit: a unit never crosses a page
-constexpr int kStages = 3;            // of each warp's ring
-constexpr int kStageBytes = 8192;     // K and V rows of one step of a warp
-constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
-constexpr int kCtas = kDecCtas;
+constexpr int kUnit = 16;  // keys of a unit: a unit never crosses a page
+
+// Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
+// A stage of a warp's ring holds the K and V rows of one unit.
+template <int DH, bool FP8, int NT>
+struct Variant {
+    static constexpr int R = 8 * NT;
+    static constexpr int RB = DH * (FP8 ? 1 : 2);
+    static constexpr int STAGE = 2 * kUnit * RB;
+    static constexpr int STAGES = RB == 256 ? 3 : NT == 4 ? 5 : 4;
+    static constexpr int RING = STAGES * STAGE;             // of one warp
+    static constexpr int SMEM = kWarps * RING;
+    static constexpr int PER_SM = RB == 256 || NT > 1 ? 2 : 3;  // CTAs (shared memory and registers)
+    static constexpr int CTAS = 148 * PER_SM;
+    static constexpr int OS = DH + 4;                       // row stride of the warps' join
+    static_assert(R * OS * 4 <= RING, "a warp's partial rows fit its ring");
+    static_assert(CTAS <= kDecCtas && R <= kDecRows, "workspace");
+};
+
 // Weights are taken relative to m = (largest z when m was set) - kLift and may
 // grow to 2^kRoof before m moves: no maximum has to be found in most steps.
 // fp16 weights then span 2^kRoof (its largest is just under 2^16) down to
@@ -159,56 +174,59 @@ __device__ __forceinline__ int out_col(int mt, int i, int g) {
 }
 
 template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
-    constexpr int R = 8 * NT;                       // packed rows of a tile
-    constexpr int RB = DH * (FP8 ? 1 : 2);          // bytes of a head's row
-    constexpr int CPR = RB / 16;                    // 16-byte chunks of it
-    constexpr int KS = kStageBytes / (2 * kUnit * RB);  // units of a step
+__global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode_kernel(DecodeParams D) {
+    using V = Variant<DH, FP8, NT>;
+    constexpr int R = V::R, RB = V::RB, OS = V::OS, STAGES = V::STAGES;
+    constexpr int CPR = RB / 16;                    // 16-byte chunks of a row
     constexpr int QS = RB / 32;                     // k-steps of the first product
     constexpr int MT = DH / 16;                     // row blocks of the second
     constexpr int LROWS = 32 / CPR;                 // rows that a warp copies at once
-    constexpr int OS = DH + 4;                      // row stride of the join in shared memory
-    static_assert(R * OS * 4 <= kStages * kStageBytes, "a warp's partial rows fit its ring");
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ long long sums[kWarps];
     __shared__ int start_seq;
-    __shared__ long long start_base;
+    __shared__ long long start_base, chunk_end;
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
+    __shared__ float2 sm_fac[kWarps][STAGES];       // K, V scale factors of the unit in a stage
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    const uint32_t my_ring = smem_u32(ring) + warp * kStages * kStageBytes;
+    uint8_t* const my_ring = ring + warp * V::RING;
+    const uint32_t my_smem = smem_u32(my_ring);
+    wait_previous();
+    allow_next();
 
-    // total units, and this CTA's share of them
-    long long total = 0;
-    for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
+    // total units, this CTA's share of them, and the sequence that holds its first
+    const int c = blockIdx.x;
+    if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
+    long long total = 0, n = threadIdx.x < p.num_seqs ? seq_units<R>(p, threadIdx.x) : 0;
+    long long at = block_prefix(n, total, sums);
+    for (int b0 = kThreads; b0 < p.num_seqs; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         long long t;
         block_prefix(b < p.num_seqs ? seq_units<R>(p, b) : 0, t, sums);
         total += t;
     }
-    // a share is at least one step of each warp
-    const long long want = (total + kWarps * KS - 1) / (kWarps * KS);
+    // a share is at least one unit of each warp
+    const long long want = (total + kWarps - 1) / kWarps;
     const int ctas = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
-    const int c = blockIdx.x;
-    if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
     if (c >= ctas || total == 0) return;
     auto share = [&](int i) { return total * i / ctas; };
     long long u = share(c);
     const long long u_end = share(c + 1);
-
-    // the sequence that holds unit u
-    long long base = 0;
-    for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        long long t;
-        const long long n = b < p.num_seqs ? seq_units<R>(p, b) : 0;
-        const long long at = base + block_prefix(n, t, sums);
+    for (int b0 = 0;;) {
         if (n > 0 && at <= u && u < at + n) {
-            start_seq = b;
+            start_seq = b0 + threadIdx.x;
             start_base = at;
         }
-        base += t;
+        if ((b0 += kThreads) >= p.num_seqs) break;
+        const int b = b0 + threadIdx.x;
+        // (the next chunk's sequences start where this chunk's end)
+        if (threadIdx.x == kThreads - 1) chunk_end = at + n;
+        __syncthreads();
+        const long long base = chunk_end;
+        long long t;
+        n = b < p.num_seqs ? seq_units<R>(p, b) : 0;
+        at = base + block_prefix(n, t, sums);
     }
     __syncthreads();
     int b = start_seq;
@@ -238,43 +256,61 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
         const int seen_all = s.P + t_first + 1;  // keys that every row of the tile sees
         const int seen_any = s.P + t_last + 1;   // keys past it are not read
 
-        // ---- the copies of this warp: steps of KS units, kWarps * KS apart ----
-        const int first = x0 + warp * KS;
-        const int steps = x1 > first ? (x1 - first + kWarps * KS - 1) / (kWarps * KS) : 0;
-        int row_reg = -1;  // lane i: cache row where unit 32 * (n / 32) + i of this warp starts
-        auto unit_at = [&](int n) { return first + (n / KS) * (kWarps * KS) + n % KS; };
-        auto load_rows = [&](int n0) {
-            const int x = unit_at(n0 + lane);
-            row_reg = x < x1 && x * kUnit < seen_any ? (int)key_row(p, s, b, x * kUnit) : -1;
+        // ---- the copies of this warp: its units are kWarps apart ----
+        const int first = x0 + warp;
+        const int steps = x1 > first ? (x1 - first + kWarps - 1) / kWarps : 0;
+        // lane i: cache row where unit 32 k + i of this warp starts, and the
+        // unit's factors; loaded a round of 32 units ahead of their use
+        int row_now, row_next;
+        float2 fac_now, fac_next;
+        auto load_round = [&](int n0, int& row, float2& fac) {
+            const int x = first + (n0 + lane) * kWarps;
+            const bool on = x < x1 && x * kUnit < seen_any;
+            row = on ? (int)key_row(p, s, b, x * kUnit) : -1;
+            fac = make_float2(1.f, 1.f);
+            if (FP8 && p.kb_fac && on) {
+                const size_t f = ((size_t)b * p.nkb_max + x * kUnit / p.B) * p.Hkv + hk;
+                fac = make_float2(p.kb_fac[f], p.vb_fac[f]);
+            }
         };
+        load_round(0, row_now, fac_now);
+        load_round(32, row_next, fac_next);
         const uint8_t* kbase = static_cast<const uint8_t*>(D.k) + (size_t)hk * RB + (lane % CPR) * 16;
         const uint8_t* vbase = static_cast<const uint8_t*>(D.v) + (size_t)hk * RB + (lane % CPR) * 16;
         const long long token = (long long)p.Hkv * RB;  // bytes between two tokens' rows
-        auto issue = [&](int i) {
+        const long long lane_row = (lane / CPR) * token;
+        auto issue = [&](int i, int stage) {
             if (i < steps) {
-                const uint32_t dst = my_ring + (i % kStages) * kStageBytes;
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    const int n = i * KS + kk;
-                    if ((n & 31) == 0) load_rows(n);
-                    const int row0 = __shfl_sync(~0u, row_reg, n & 31);
-                    const int valid = row0 < 0 ? 0 : min(kUnit, seen_any - unit_at(n) * kUnit);
-                    const long long at = (long long)max(row0, 0) * token;
-#pragma unroll
-                    for (int r0 = 0; r0 < kUnit; r0 += LROWS) {
-                        const int r = r0 + lane / CPR;
-                        const uint32_t to = dst + (kk * kUnit + r) * RB + (((lane % CPR) ^ (r & 7)) << 4);
-                        const bool on = r < valid;
-                        const long long off = on ? at + r * token : 0;
-                        copy16(to, kbase + off, on);
-                        copy16(to + kStageBytes / 2, vbase + off, on);
+                if (i > 0 && (i & 31) == 0) {
+                    row_now = row_next;
+                    fac_now = fac_next;
+                    load_round(i + 32, row_next, fac_next);
+                }
+                const uint32_t dst = my_smem + stage * V::STAGE;
+                const int row0 = __shfl_sync(~0u, row_now, i & 31);
+                const int valid = row0 < 0 ? 0 : seen_any - (first + i * kWarps) * kUnit;
+                if (FP8 && p.kb_fac && lane == (i & 31)) {
+                    if (!(fac_now.x > 0.f && fac_now.x <= 1.f && fac_now.y > 0.f && fac_now.y <= 1.f)) {
+                        set_error(p.err, kErrInvalid, kDetFactor);
+                        fac_now = make_float2(1.f, 1.f);
                     }
+                    sm_fac[warp][stage] = fac_now;
+                }
+                const long long from = (long long)max(row0, 0) * token + lane_row;
+#pragma unroll
+                for (int r0 = 0; r0 < kUnit; r0 += LROWS) {
+                    const int r = r0 + lane / CPR;
+                    const uint32_t to = dst + r * RB + (((lane % CPR) ^ (r & 7)) << 4);
+                    const bool on = r < valid;
+                    const long long off = on ? from + r0 * token : 0;
+                    copy16(to, kbase + off, on);
+                    copy16(to + V::STAGE / 2, vbase + off, on);
                 }
             }
             copies_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(i);
+        for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
 
         // ---- this warp's query columns, running (m, l, o) ----
         uint32_t qf[NT][QS][2];
@@ -305,105 +341,100 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
                 for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
         }
 
+        int stage = 0, fill = STAGES - 1;
         for (int i = 0; i < steps; ++i) {
-            copies_wait<kStages - 2>();
+            copies_wait<STAGES - 2>();
             __syncwarp();
-            issue(i + kStages - 1);
-            const uint32_t ks0 = my_ring + (i % kStages) * kStageBytes, vs0 = ks0 + kStageBytes / 2;
-            float z[KS][NT][4];
+            issue(i + STAGES - 1, fill);
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            const uint32_t ks0 = my_smem + stage * V::STAGE, vs0 = ks0 + V::STAGE / 2;
+            const int j0 = (first + i * kWarps) * kUnit;
+            float z[NT][4];  // S^T: key g (+ 8 for 2, 3), rows 2 t4, 2 t4 + 1
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z[kk][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
+            {
                 const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
                 for (int ks = 0; ks < QS; ++ks) {
                     uint32_t a[4];
-                    ldsm4(a, ks0 + (kk * kUnit + r) * RB + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
+                    ldsm4(a, ks0 + r * RB + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (FP8) mma_e4m3(z[kk][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-                        else mma_bf16(z[kk][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                        if constexpr (FP8) mma_e4m3(z[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                        else mma_bf16(z[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
                     }
                 }
             }
-            float fv[KS];
-            bool grow = false;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                const int n = i * KS + kk, x = unit_at(n), j0 = x * kUnit;
-                float fk = 1.f;
-                fv[kk] = 1.f;
-                const bool past = x >= x1;  // beyond the share: another CTA's keys
-                if constexpr (FP8) {
-                    if (p.kb_fac && x < x1) {
-                        const size_t at = ((size_t)b * p.nkb_max + j0 / p.B) * p.Hkv + hk;
-                        fk = p.kb_fac[at];
-                        fv[kk] = p.vb_fac[at];
-                        if (!(fk > 0.f && fk <= 1.f && fv[kk] > 0.f && fv[kk] <= 1.f)) {
-                            set_error(p.err, kErrInvalid, kDetFactor);
-                            fk = fv[kk] = 1.f;
-                        }
-                    }
-                }
+            float2 fac = make_float2(1.f, 1.f);
+            if (FP8 && p.kb_fac) fac = sm_fac[warp][stage];
+            if (j0 + kUnit > seen_all) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y = z[kk][nt][e] * (FP8 ? sc[nt][e & 1] * fk : sc[nt][e & 1]);
-                        if (j0 + kUnit > seen_all || past)
-                            if (past || j0 + g + (e >> 1) * 8 > last[nt][e & 1]) y = -INFINITY;
-                        z[kk][nt][e] = y;
-                        grow |= y - m[nt][e & 1] > kRoof;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (j0 + g + (e >> 1) * 8 > last[nt][e & 1]) z[nt][e] = -INFINITY;
             }
+            // exponents of the weights; m moves when one passes the roof
+            float w[NT][4];
+            bool grow = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[nt][e] = fmaf(z[nt][e], FP8 ? sc[nt][e & 1] * fac.x : sc[nt][e & 1], -m[nt][e & 1]);
+                    grow |= w[nt][e] > kRoof;
+                }
             if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y = -INFINITY;
-#pragma unroll
-                        for (int kk = 0; kk < KS; ++kk) y = fmaxf(y, fmaxf(z[kk][nt][e], z[kk][nt][e + 2]));
+                        const float f = FP8 ? sc[nt][e] * fac.x : sc[nt][e];
+                        float y = fmaxf(z[nt][e] * f, z[nt][e + 2] * f);
                         y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
                         if (y - m[nt][e] > kRoof) {
-                            const float f = ex2(m[nt][e] - (y - kLift));
+                            const float shrink = ex2(m[nt][e] - (y - kLift));
                             m[nt][e] = y - kLift;
-                            l[nt][e] *= f;
+                            l[nt][e] *= shrink;
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
-                                o[nt][mt][e] *= f;
-                                o[nt][mt][e + 2] *= f;
+                                o[nt][mt][e] *= shrink;
+                                o[nt][mt][e + 2] *= shrink;
                             }
                         }
+                        w[nt][e] = fmaf(z[nt][e], f, -m[nt][e]);
+                        w[nt][e + 2] = fmaf(z[nt][e + 2], f, -m[nt][e]);
                     }
             }
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
+            {
                 // weights as the 16-bit operand: fp16 (11 bits) beside e4m3 values;
                 // beside bf16 ones two bf16 terms (16 bits), so that the weights'
                 // rounding stays far below the output's
                 uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = ex2(z[kk][nt][e] - m[nt][e & 1]);
-                    l[nt][0] += w[0] + w[2];
-                    l[nt][1] += w[1] + w[3];
+                    for (int e = 0; e < 4; ++e) w[nt][e] = ex2(w[nt][e]);
+                    l[nt][0] += w[nt][0] + w[nt][2];
+                    l[nt][1] += w[nt][1] + w[nt][3];
+                    if (FP8 && p.kb_fac) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[nt][e] *= fac.y;
+                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        const float x = w[nt][2 * e], y = w[nt][2 * e + 1];
                         if constexpr (FP8) {
-                            hi[nt][e] = transpose8(pack_f16x2(w[2 * e] * fv[kk], w[2 * e + 1] * fv[kk]));
+                            hi[nt][e] = transpose8(pack_f16x2(x, y));
                         } else {
-                            const uint32_t x = pack_bf16x2(w[2 * e], w[2 * e + 1]);
-                            hi[nt][e] = transpose8(x);
-                            lo[nt][e] = transpose8(pack_bf16x2(w[2 * e] - __uint_as_float(x << 16),
-                                                               w[2 * e + 1] - __uint_as_float(x & 0xFFFF0000u)));
+                            const uint32_t h = pack_bf16x2(x, y);
+                            hi[nt][e] = transpose8(h);
+                            lo[nt][e] = transpose8(
+                                pack_bf16x2(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xFFFF0000u)));
                         }
                     }
                 }
@@ -412,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
                         // one load covers two products: 16 keys x 32 values
                         uint32_t v[4];
                         const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
-                        ldsm4_t(v, vs0 + (kk * kUnit + r) * RB + ((((mt & ~1) + (lane >> 4)) ^ (r & 7)) << 4));
+                        ldsm4_t(v, vs0 + r * RB + ((((mt & ~1) + (lane >> 4)) ^ (r & 7)) << 4));
                         const uint32_t x = __byte_perm(v[2 * (mt & 1)], 0, 0x3120), y = __byte_perm(v[2 * (mt & 1) + 1], 0, 0x3120);
                         a[0] = f16_of((uint16_t)x);
                         a[1] = f16_of((uint16_t)(x >> 16));
@@ -420,10 +451,9 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
                         a[3] = f16_of((uint16_t)(y >> 16));
                     } else {
                         const int r = (lane & 7) + (lane >> 4) * 8;
-                        ldsm4_t(a, vs0 + (kk * kUnit + r) * RB + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+                        ldsm4_t(a, vs0 + r * RB + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
                     }
                 };
-                const int j0 = unit_at(i * KS + kk) * kUnit;
                 if (t_first == t_last || j0 + kUnit <= seen_all) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
@@ -447,7 +477,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
                     for (int tok = t_last; tok >= t_first; --tok) {
                         const int clear = max(0, s.P + tok + 1 - j0);
                         for (int y = clear * CPR + lane; y < kUnit * CPR; y += 32)
-                            *reinterpret_cast<uint4*>(ring + (vs0 - smem_u32(ring)) + (kk * kUnit) * RB + y * 16) =
+                            *reinterpret_cast<uint4*>(my_ring + (vs0 - my_smem) + y * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         __syncwarp();
 #pragma unroll
@@ -472,12 +502,13 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
                     }
                 }
             }
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
         }
         copies_wait<0>();
         __syncwarp();
 
         // ---- the warps' parts of this segment, joined in shared memory ----
-        float* mine = reinterpret_cast<float*>(ring + warp * kStages * kStageBytes);
+        float* mine = reinterpret_cast<float*>(my_ring);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -509,7 +540,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ex2(sm_m[w][r] - M);
                 L += f * sm_l[w][r];
-                O += f * reinterpret_cast<const float*>(ring + w * kStages * kStageBytes)[r * OS + col];
+                O += f * reinterpret_cast<const float*>(ring + w * V::RING)[r * OS + col];
             }
             const int tok = (tile * R + r) / p.G, h = hk * p.G + (tile * R + r) % p.G;
             if (whole) {
@@ -536,36 +567,67 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams D) {
     }
 }
 
-// grid (shares, R), DH threads: row r of the item that starts in share c and
-// ends in a later one.
+// grid (shares, R): row r of the item that starts in share c and ends in a
+// later one.  A warp adds up every kJoinWarps-th part, DH / 32 columns a lane.
+constexpr int kJoinWarps = 8;
 template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(DH) join_kernel(DecodeParams D) {
-    constexpr int R = 8 * NT;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(DecodeParams D) {
+    constexpr int R = 8 * NT, E = DH / 32;
+    __shared__ float sm_o[kJoinWarps][DH], sm_m[kJoinWarps], sm_l[kJoinWarps];
+    wait_previous();
+    allow_next();
     const KParams& p = D.p;
-    const int c = blockIdx.x, r = blockIdx.y, col = threadIdx.x;
+    const int c = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int4 rec = D.record[2 * c];
     if (rec.x == 0) return;
     if (r >= D.record[2 * c + 1].x) return;
     auto slot = [&](int i) { return ((size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R + r); };
-    float M = -FLT_MAX, L = 0.f, O = 0.f;
-    for (int i = 0; i < rec.x; ++i) M = fmaxf(M, D.part_ml[2 * slot(i)]);
-    for (int i = 0; i < rec.x; ++i) {
-        const float f = ex2(D.part_ml[2 * slot(i)] - M);
-        L += f * D.part_ml[2 * slot(i) + 1];
-        O += f * D.part[slot(i) * DH + col];
+    float M = -FLT_MAX, L = 0.f, O[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) O[e] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < rec.x; i += kJoinWarps) {
+        const float2 ml = *reinterpret_cast<const float2*>(D.part_ml + 2 * slot(i));
+        const float* part = D.part + slot(i) * DH + lane * E;
+        const float mn = fmaxf(M, ml.x), old = ex2(M - mn), f = ex2(ml.x - mn);
+        M = mn;
+        L = L * old + ml.y * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] = O[e] * old + part[e] * f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = O[e];
+    if (lane == 0) {
+        sm_m[warp] = M;
+        sm_l[warp] = L;
+    }
+    __syncthreads();
+    const int col = threadIdx.x;
+    if (col >= DH) return;
+    M = -FLT_MAX;
+    L = 0.f;
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, sm_m[w]);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ex2(sm_m[w] - M);
+        L += f * sm_l[w];
+        o += f * sm_o[w][col];
     }
     const int t = (rec.w * R + r) / p.G, h = rec.z * p.G + (rec.w * R + r) % p.G;
-    put_out(D, rec.y + t, h, col, O * ((FP8 ? p.v_scale[rec.z] : 1.f) / L));
+    put_out(D, rec.y + t, h, col, o * ((FP8 ? p.v_scale[rec.z] : 1.f) / L));
     if (D.lse && col == 0) D.lse[(long long)(rec.y + t) * p.Hq + h] = lse_of(M, L);
 }
 
 template <int DH, bool FP8, int NT>
 cudaError_t launch(const DecodeParams& D, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<DH, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    decode_kernel<DH, FP8, NT><<<kCtas, kThreads, kSmemBytes, s>>>(D);
-    join_kernel<DH, FP8, NT><<<dim3(kCtas, 8 * NT), DH, 0, s>>>(D);
-    return cudaGetLastError();
+    using V = Variant<DH, FP8, NT>;
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = allow_smem(decode_kernel<DH, FP8, NT>, V::SMEM, ready);
+    if (e == cudaSuccess) e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D);
+    if (e == cudaSuccess) e = launch_early(join_kernel<DH, FP8, NT>, dim3(V::CTAS, V::R), 32 * kJoinWarps, 0, s, D);
+    return e;
 }
 
 template <int DH, bool FP8>

@@ -116,7 +116,7 @@ struct DecodeParams {
     int4* record;              // [kDecCtas][2]: what the join kernel has to do
     float qk_scale;            // log2(e) / sqrt(d)
 };
-constexpr int kDecCtas = 296;  // CTAs of the split: 2 on each of 148 SMs
+constexpr int kDecCtas = 444;  // most CTAs of the split: 3 on each of 148 SMs
 constexpr int kDecRows = 32;   // most packed query rows (tokens x group heads) of a tile
 
 cudaError_t launch_page_map(const MapParams& p, cudaStream_t s);

@@ -463,8 +463,11 @@ class _Step:
         import torch
         self.device = torch.device(device)
         self._stream = stream
-        self._current = torch.cuda.current_stream
-        self._current_device = torch.cuda.current_device
+        # the raw handle and the device index, without the objects around them:
+        # a step of single tokens is a few microseconds long
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._raw_device = torch._C._cuda_getDevice
+        self._index = self.device.index
         self._guard = torch.cuda.device
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -481,16 +484,14 @@ class _Step:
 
     def _on_stream(self):
         s = self._stream
-        self.params.stream = self._current(self.device).cuda_stream if s is None else s
+        self.params.stream = self._raw_stream(self._index) if s is None else s
 
     def run(self) -> None:
-        if self._current_device() != self.device.index:
+        if self._raw_device() != self._index:
             with self._guard(self.device):
-                return self._launch()
-        return self._launch()
-
-    def _launch(self) -> None:
-        self._on_stream()
+                return self.run()
+        s = self._stream
+        self.params.stream = self._raw_stream(self._index) if s is None else s
         st = self._fn(*self._args)
         if st != FP2_OK:
             raise Fp2Error(st, self._name)
