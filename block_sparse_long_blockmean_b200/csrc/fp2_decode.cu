@@ -7,12 +7,12 @@
 // (m, l, o).  Two disjoint key ranges join by m = max(m1, m2), l = l1 2^(m1-m)
 // + l2 2^(m2-m), o likewise; out = o / l, lse = ln 2 (m + log2 l).
 //
-// Split: the unit of work is 16 keys of one (sequence, KV head, row tile).  All
-// units, in that order, are cut into equal shares, one per CTA, so lengths may
-// differ at will; every CTA finds its own share from the lengths.  An item
-// (sequence, head, tile) that lies in one share is finished there; one that
-// spans several leaves a partial (m, l, o) per share in the workspace and the
-// join kernel reduces them.
+// Split: the unit of work is 16 keys of one (sequence, group of hc adjacent KV
+// heads, row tile).  All units, in that order, are cut into equal shares, one
+// per CTA, so lengths may differ at will; every CTA finds its own share from the
+// lengths.  An item (sequence, head group, tile) that lies in one share is
+// finished there; one that spans several leaves a partial (m, l, o) per share in
+// the workspace and a join kernel reduces them.
 //
 // Products: both on the tensor core with the keys (or the head dimension) as
 // the 16 rows of an m16n8 product and 8 packed query rows as its columns:
@@ -37,7 +37,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = 16;  // keys of a unit: a unit never crosses a page
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
-// A stage of a warp's ring holds the K and V rows of one unit.
+// A stage of a warp's ring holds the K and V rows of one unit and head.
 template <int DH, bool FP8, int NT>
 struct Variant {
     static constexpr int R = 8 * NT;
@@ -62,21 +62,26 @@ constexpr float kLift = 7.f, kRoof = 15.f;
 struct Shape {
     long long units;  // of the sequence
     int per_item;     // units of one item: ceil(Lk / kUnit)
-    int tiles;        // row tiles per head
+    int tiles;        // row tiles per head group
 };
 template <int R>
-__device__ __forceinline__ Shape seq_shape(const KParams& p, const SeqInfo& s) {
+__device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const SeqInfo& s) {
     Shape x;
     x.per_item = (s.Lk + kUnit - 1) / kUnit;
-    x.tiles = (s.Lq * p.G + R - 1) / R;
-    x.units = (long long)x.per_item * x.tiles * p.Hkv;
+    x.tiles = (s.Lq * D.p.G + R - 1) / R;
+    x.units = (long long)x.per_item * x.tiles * D.groups;
     return x;
 }
+// Sequence b's lengths and its units; 0 units if it rests or its lengths are bad.
 template <int R>
-__device__ __forceinline__ long long seq_units(const KParams& p, int b) {
-    SeqInfo s;
-    if (!load_seq(p, b, s) || s.Lq == 0) return 0;
-    return seq_shape<R>(p, s).units;
+__device__ __forceinline__ long long seq_units(const DecodeParams& D, int b, SeqInfo& s) {
+    if (!load_seq(D.p, b, s) || s.Lq == 0) return 0;
+    return seq_shape<R>(D, s).units;
+}
+// a / b of values that mostly fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
 }
 
 // Sum of x over the CTA and the exclusive prefix of the calling thread.
@@ -101,20 +106,27 @@ __device__ __forceinline__ long long block_prefix(long long x, long long& total,
     return before + y - x;
 }
 
-// Output of one packed row: o (unnormalised) over l, rounded once.
-__device__ __forceinline__ void put_out(const DecodeParams& D, long long row, int h, int col, float x) {
+// Four columns of one packed row's output, rounded once.
+__device__ __forceinline__ void put_out(const DecodeParams& D, long long row, int h, int col, float4 x) {
     const KParams& p = D.p;
     const long long at = (row * p.Hq + h) * p.d + col;
     if (p.out_fp8) {
         const float sc = p.out_scale ? p.out_scale[h] : p.v_scale[h / p.G];
-        const uint32_t b = pack_e4m3x4(x / sc, 0.f, 0.f, 0.f);
-        static_cast<uint8_t*>(D.out)[at] = (uint8_t)b;
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D.out) + at) = pack_e4m3x4(x.x / sc, x.y / sc, x.z / sc, x.w / sc);
     } else {
-        static_cast<__nv_bfloat16*>(D.out)[at] = __float2bfloat16(x);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(D.out) + at) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     }
 }
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
+__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+__device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b f
+    return make_float4(fmaf(b.x, f, a.x), fmaf(b.y, f, a.y), fmaf(b.z, f, a.z), fmaf(b.w, f, a.w));
+}
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes to shared memory, zeros where !on (then nothing is read).
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -130,6 +142,12 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
 }
 __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// Two 16 x 16 byte matrices, transposed: register 2 k + i of lane l holds bytes
+// 4 (l % 4) .. + 3 of column l / 4 + 8 i of matrix k.
+__device__ __forceinline__ void ldsm_bytes_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -153,9 +171,12 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Two e4m3 -> two fp16, exact.
-__device__ __forceinline__ uint32_t f16_of(uint16_t x) {
+__device__ __forceinline__ uint32_t f16_of(uint32_t x, bool high) {
     uint32_t y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    if (high)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
@@ -164,59 +185,80 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     return d;
 }
 
-// The rows of V^T that product mt of O^T covers: bf16 16 consecutive ones in
-// natural order; e4m3 (two values per 16-bit element of the transposing load)
-// the even ones first.  Column of the head for accumulator pair i (0: rows
-// 0-7 of the product, 1: rows 8-15) of lane group g.
+// Key of row i of S^T within its unit.  bf16: i.  e4m3: the byte transpose of V
+// puts keys 4 t .. 4 t + 3 into one register, which as 16-bit operands are the
+// product's k = 2 t, 2 t + 1 and 2 t + 8, 2 t + 9; S^T takes its keys in that
+// order, so that no byte of V has to move.
 template <bool FP8>
-__device__ __forceinline__ int out_col(int mt, int i, int g) {
-    return 16 * mt + (FP8 ? 2 * g + i : 8 * i + g);
+__device__ __forceinline__ int key_of(int i) {
+    return FP8 ? 4 * ((i & 7) >> 1) + (i & 1) + 2 * (i >> 3) : i;
+}
+// The 16-byte chunks of a K row are stored at chunk ^ this, of a V row at chunk
+// ^ (row & 7): the 8 rows of a matrix load then lie in different banks.
+template <bool FP8>
+__device__ __forceinline__ int k_swizzle(int row) {
+    return FP8 ? (row & 1) | ((row >> 2) & 3) << 1 : row & 7;
 }
 
 template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode_kernel(DecodeParams D) {
+__global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode_kernel(const __grid_constant__ DecodeParams D) {
     using V = Variant<DH, FP8, NT>;
     constexpr int R = V::R, RB = V::RB, OS = V::OS, STAGES = V::STAGES;
-    constexpr int CPR = RB / 16;                    // 16-byte chunks of a row
-    constexpr int QS = RB / 32;                     // k-steps of the first product
-    constexpr int MT = DH / 16;                     // row blocks of the second
-    constexpr int LROWS = 32 / CPR;                 // rows that a warp copies at once
+    constexpr int CPR = RB / 16;     // 16-byte chunks of a row
+    constexpr int QS = RB / 32;      // k-steps of the first product
+    constexpr int MT = DH / 16;      // row blocks of the second
+    constexpr int LROWS = 32 / CPR;  // rows that a warp copies at once
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ long long sums[kWarps];
     __shared__ int start_seq;
+    __shared__ SeqInfo start_info;
     __shared__ long long start_base, chunk_end;
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
-    __shared__ float2 sm_fac[kWarps][STAGES];       // K, V scale factors of the unit in a stage
+    __shared__ float2 sm_fac[kWarps][STAGES];  // K, V scale factors of the unit in a stage
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
+    // warp = head of the group + hc * (which of the kw warps that share its units)
+    const int hs = warp % D.hc, kw = kWarps / D.hc;
     uint8_t* const my_ring = ring + warp * V::RING;
     const uint32_t my_smem = smem_u32(my_ring);
+    const int c = blockIdx.x;
     wait_previous();
     allow_next();
 
     // total units, this CTA's share of them, and the sequence that holds its first
-    const int c = blockIdx.x;
-    if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
-    long long total = 0, n = threadIdx.x < p.num_seqs ? seq_units<R>(p, threadIdx.x) : 0;
+    SeqInfo s;
+    long long total = 0, n = threadIdx.x < p.num_seqs ? seq_units<R>(D, threadIdx.x, s) : 0;
     long long at = block_prefix(n, total, sums);
     for (int b0 = kThreads; b0 < p.num_seqs; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         long long t;
-        block_prefix(b < p.num_seqs ? seq_units<R>(p, b) : 0, t, sums);
+        SeqInfo x;
+        block_prefix(b < p.num_seqs ? seq_units<R>(D, b, x) : 0, t, sums);
         total += t;
     }
+    if (!D.few) {
+        if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
+    } else if (c == 0 && threadIdx.x < p.num_seqs) {
+        // (few: a record per item, at most as many sequences as threads; the
+        // tiles that this sequence does not have)
+        const int tiles = n > 0 ? seq_shape<R>(D, s).tiles : 0;
+        for (int i = 0; i < D.groups; ++i)
+            for (int j = tiles; j < D.tiles_max; ++j)
+                D.record[2 * ((threadIdx.x * D.groups + i) * D.tiles_max + j)] = make_int4(0, 0, 0, 0);
+    }
     // a share is at least one unit of each warp
-    const long long want = (total + kWarps - 1) / kWarps;
+    const long long want = (total + kw - 1) / kw;
     const int ctas = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
     if (c >= ctas || total == 0) return;
-    auto share = [&](int i) { return total * i / ctas; };
+    auto share = [&](int i) { return quotient(total * i, ctas); };
     long long u = share(c);
     const long long u_end = share(c + 1);
     for (int b0 = 0;;) {
         if (n > 0 && at <= u && u < at + n) {
             start_seq = b0 + threadIdx.x;
             start_base = at;
+            start_info = s;
         }
         if ((b0 += kThreads) >= p.num_seqs) break;
         const int b = b0 + threadIdx.x;
@@ -225,28 +267,27 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
         __syncthreads();
         const long long base = chunk_end;
         long long t;
-        n = b < p.num_seqs ? seq_units<R>(p, b) : 0;
+        n = b < p.num_seqs ? seq_units<R>(D, b, s) : 0;
         at = base + block_prefix(n, t, sums);
     }
     __syncthreads();
     int b = start_seq;
     long long seq_at = start_base;
+    s = start_info;
 
-    while (u < u_end && b < p.num_seqs) {
-        SeqInfo s;
-        if (!load_seq(p, b, s) || s.Lq == 0) {
-            ++b;
-            continue;
-        }
-        const Shape sh = seq_shape<R>(p, s);
-        if (u >= seq_at + sh.units) {
+    while (u < u_end) {
+        Shape sh = seq_shape<R>(D, s);
+        while (u >= seq_at + sh.units) {  // on to the sequence that holds u
             seq_at += sh.units;
-            ++b;
-            continue;
+            do
+                if (++b >= p.num_seqs) return;
+            while (!load_seq(p, b, s) || s.Lq == 0);
+            sh = seq_shape<R>(D, s);
         }
-        const int item = (int)((u - seq_at) / sh.per_item);
+        const int item = (int)quotient(u - seq_at, sh.per_item);
         const long long item_at = seq_at + (long long)item * sh.per_item;
-        const int hk = item / sh.tiles, tile = item % sh.tiles;
+        const int group = item / sh.tiles, tile = item % sh.tiles;
+        const int hk = group * D.hc + hs;
         const int x0 = (int)(u - item_at);
         const int x1 = (int)min((long long)sh.per_item, u_end - item_at);
 
@@ -256,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
         const int seen_all = s.P + t_first + 1;  // keys that every row of the tile sees
         const int seen_any = s.P + t_last + 1;   // keys past it are not read
 
-        // ---- the copies of this warp: its units are kWarps apart ----
-        const int first = x0 + warp;
-        const int steps = x1 > first ? (x1 - first + kWarps - 1) / kWarps : 0;
+        // ---- the copies of this warp: its units are kw apart ----
+        const int first = x0 + warp / D.hc;
+        const int steps = x1 > first ? (x1 - first + kw - 1) / kw : 0;
         // lane i: cache row where unit 32 k + i of this warp starts, and the
         // unit's factors; loaded a round of 32 units ahead of their use
         int row_now, row_next;
         float2 fac_now, fac_next;
         auto load_round = [&](int n0, int& row, float2& fac) {
-            const int x = first + (n0 + lane) * kWarps;
+            const int x = first + (n0 + lane) * kw;
             const bool on = x < x1 && x * kUnit < seen_any;
             row = on ? (int)key_row(p, s, b, x * kUnit) : -1;
             fac = make_float2(1.f, 1.f);
@@ -275,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
         };
         load_round(0, row_now, fac_now);
         load_round(32, row_next, fac_next);
-        const uint8_t* kbase = static_cast<const uint8_t*>(D.k) + (size_t)hk * RB + (lane % CPR) * 16;
-        const uint8_t* vbase = static_cast<const uint8_t*>(D.v) + (size_t)hk * RB + (lane % CPR) * 16;
         const long long token = (long long)p.Hkv * RB;  // bytes between two tokens' rows
-        const long long lane_row = (lane / CPR) * token;
+        const long long lane_at = hk * RB + (lane % CPR) * 16 + (lane / CPR) * token;
+        const uint8_t* const kbase = static_cast<const uint8_t*>(D.k) + lane_at;
+        const long long k_to_v = static_cast<const uint8_t*>(D.v) - static_cast<const uint8_t*>(D.k);
         auto issue = [&](int i, int stage) {
             if (i < steps) {
                 if (i > 0 && (i & 31) == 0) {
@@ -286,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                     fac_now = fac_next;
                     load_round(i + 32, row_next, fac_next);
                 }
-                const uint32_t dst = my_smem + stage * V::STAGE;
+                const uint32_t dst = my_smem + stage * V::STAGE + lane / CPR * RB;
                 const int row0 = __shfl_sync(~0u, row_now, i & 31);
-                const int valid = row0 < 0 ? 0 : seen_any - (first + i * kWarps) * kUnit;
+                const int valid = row0 < 0 ? 0 : seen_any - (first + i * kw) * kUnit;
                 if (FP8 && p.kb_fac && lane == (i & 31)) {
                     if (!(fac_now.x > 0.f && fac_now.x <= 1.f && fac_now.y > 0.f && fac_now.y <= 1.f)) {
                         set_error(p.err, kErrInvalid, kDetFactor);
@@ -296,15 +337,21 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                     }
                     sm_fac[warp][stage] = fac_now;
                 }
-                const long long from = (long long)max(row0, 0) * token + lane_row;
+                const uint8_t* from = kbase + max(row0, 0) * token;
 #pragma unroll
-                for (int r0 = 0; r0 < kUnit; r0 += LROWS) {
+                for (int r0 = 0; r0 < kUnit; r0 += LROWS, from += LROWS * token) {
                     const int r = r0 + lane / CPR;
-                    const uint32_t to = dst + r * RB + (((lane % CPR) ^ (r & 7)) << 4);
-                    const bool on = r < valid;
-                    const long long off = on ? from + r0 * token : 0;
-                    copy16(to, kbase + off, on);
-                    copy16(to + V::STAGE / 2, vbase + off, on);
+                    const uint32_t kto = dst + r0 * RB + (((lane % CPR) ^ k_swizzle<FP8>(r)) << 4);
+                    const uint32_t vto = dst + r0 * RB + (((lane % CPR) ^ (r & 7)) << 4) + V::STAGE / 2;
+                    if (valid >= kUnit) {
+                        copy16(kto, from);
+                        copy16(vto, from + k_to_v);
+                    } else {
+                        const bool on = r < valid;
+                        const uint8_t* x = on ? from : static_cast<const uint8_t*>(D.k);
+                        copy16(kto, x, on);
+                        copy16(vto, x + k_to_v, on);
+                    }
                 }
             }
             copies_commit();
@@ -348,18 +395,18 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
             issue(i + STAGES - 1, fill);
             fill = fill + 1 == STAGES ? 0 : fill + 1;
             const uint32_t ks0 = my_smem + stage * V::STAGE, vs0 = ks0 + V::STAGE / 2;
-            const int j0 = (first + i * kWarps) * kUnit;
+            const int j0 = (first + i * kw) * kUnit;
             float z[NT][4];  // S^T: key g (+ 8 for 2, 3), rows 2 t4, 2 t4 + 1
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
             {
-                const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+                const int r = key_of<FP8>((lane & 7) + ((lane >> 3) & 1) * 8);
 #pragma unroll
                 for (int ks = 0; ks < QS; ++ks) {
                     uint32_t a[4];
-                    ldsm4(a, ks0 + r * RB + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
+                    ldsm4(a, ks0 + r * RB + (((2 * ks + (lane >> 4)) ^ k_swizzle<FP8>(r)) << 4));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         if constexpr (FP8) mma_e4m3(z[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
@@ -374,18 +421,23 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (j0 + g + (e >> 1) * 8 > last[nt][e & 1]) z[nt][e] = -INFINITY;
+                        if (j0 + key_of<FP8>(g + (e >> 1) * 8) > last[nt][e & 1]) z[nt][e] = -INFINITY;
             }
             // exponents of the weights; m moves when one passes the roof
-            float w[NT][4];
-            bool grow = false;
+            float w[NT][4], top = -FLT_MAX;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[nt][e] = fmaf(z[nt][e], FP8 ? sc[nt][e & 1] * fac.x : sc[nt][e & 1], -m[nt][e & 1]);
-                    grow |= w[nt][e] > kRoof;
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 f = make_float2(sc[nt][0], sc[nt][1]);
+                if (FP8 && p.kb_fac) f = make_float2(f.x * fac.x, f.y * fac.x);
+                const float2 shift = make_float2(-m[nt][0], -m[nt][1]);
+                const float2 x = ffma2(make_float2(z[nt][0], z[nt][1]), f, shift), y = ffma2(make_float2(z[nt][2], z[nt][3]), f, shift);
+                w[nt][0] = x.x;
+                w[nt][1] = x.y;
+                w[nt][2] = y.x;
+                w[nt][3] = y.y;
+                top = max3f(max3f(top, x.x, x.y), y.x, y.y);
+            }
+            const bool grow = top > kRoof;
             if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -419,8 +471,10 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[nt][e] = ex2(w[nt][e]);
-                    l[nt][0] += w[nt][0] + w[nt][2];
-                    l[nt][1] += w[nt][1] + w[nt][3];
+                    const float2 both = fadd2(make_float2(l[nt][0], l[nt][1]),
+                                              fadd2(make_float2(w[nt][0], w[nt][1]), make_float2(w[nt][2], w[nt][3])));
+                    l[nt][0] = both.x;
+                    l[nt][1] = both.y;
                     if (FP8 && p.kb_fac) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) w[nt][e] *= fac.y;
@@ -438,17 +492,13 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                         }
                     }
                 }
+                uint32_t pair[4];  // e4m3: one load covers two products
                 auto values = [&](int mt, uint32_t (&a)[4]) {  // V^T rows of product mt
                     if constexpr (FP8) {
-                        // one load covers two products: 16 keys x 32 values
-                        uint32_t v[4];
-                        const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
-                        ldsm4_t(v, vs0 + r * RB + ((((mt & ~1) + (lane >> 4)) ^ (r & 7)) << 4));
-                        const uint32_t x = __byte_perm(v[2 * (mt & 1)], 0, 0x3120), y = __byte_perm(v[2 * (mt & 1) + 1], 0, 0x3120);
-                        a[0] = f16_of((uint16_t)x);
-                        a[1] = f16_of((uint16_t)(x >> 16));
-                        a[2] = f16_of((uint16_t)y);
-                        a[3] = f16_of((uint16_t)(y >> 16));
+                        const int r = lane & 15;
+                        if ((mt & 1) == 0) ldsm_bytes_t(pair, vs0 + r * RB + (((mt + (lane >> 4)) ^ (r & 7)) << 4));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = f16_of(pair[2 * (mt & 1) + (e & 1)], e >= 2);
                     } else {
                         const int r = (lane & 7) + (lane >> 4) * 8;
                         ldsm4_t(a, vs0 + r * RB + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
@@ -524,77 +574,103 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    mine[r * OS + out_col<FP8>(mt, 0, g)] = o[nt][mt][e];
-                    mine[r * OS + out_col<FP8>(mt, 1, g)] = o[nt][mt][e + 2];
+                    mine[r * OS + 16 * mt + g] = o[nt][mt][e];
+                    mine[r * OS + 16 * mt + 8 + g] = o[nt][mt][e + 2];
                 }
             }
         __syncthreads();
         const bool whole = x0 == 0 && x1 == sh.per_item;
         const int slot = 2 * c + (x0 == 0 ? 1 : 0);
-        for (int y = threadIdx.x; y < rows * DH; y += kThreads) {
-            const int r = y / DH, col = y % DH;
-            float M = -FLT_MAX, L = 0.f, O = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+        for (int y = threadIdx.x; y < D.hc * rows * (DH / 4); y += kThreads) {
+            const int col = y % (DH / 4) * 4, r = y / (DH / 4) % rows, hx = y / (DH / 4) / rows;
+            float M = -FLT_MAX, L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = hx; w < kWarps; w += D.hc) M = fmaxf(M, sm_m[w][r]);
+            for (int w = hx; w < kWarps; w += D.hc) {
                 const float f = ex2(sm_m[w][r] - M);
                 L += f * sm_l[w][r];
-                O += f * reinterpret_cast<const float*>(ring + w * V::RING)[r * OS + col];
+                O = plus(O, *reinterpret_cast<const float4*>(ring + w * V::RING + (r * OS + col) * 4), f);
             }
-            const int tok = (tile * R + r) / p.G, h = hk * p.G + (tile * R + r) % p.G;
             if (whole) {
-                put_out(D, s.q0 + tok, h, col, O * ((FP8 ? p.v_scale[hk] : 1.f) / L));
+                const int tok = (tile * R + r) / p.G, hkv = group * D.hc + hx, h = hkv * p.G + (tile * R + r) % p.G;
+                put_out(D, s.q0 + tok, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
                 if (D.lse && col == 0) D.lse[(long long)(s.q0 + tok) * p.Hq + h] = lse_of(M, L);
             } else {
-                D.part[((size_t)slot * R + r) * DH + col] = O;
-                if (col == 0) {
-                    D.part_ml[((size_t)slot * R + r) * 2] = M;
-                    D.part_ml[((size_t)slot * R + r) * 2 + 1] = L;
-                }
+                const size_t at = ((size_t)slot * D.hc + hx) * R + r;
+                *reinterpret_cast<float4*>(D.part + at * DH + col) = O;
+                if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(M, L);
             }
         }
-        if (!whole && x0 == 0 && threadIdx.x == 0) {
-            // the item goes on to the share that holds its last unit
+        if (threadIdx.x == 0 && x0 == 0 && (D.few || !whole)) {
+            // an item that goes on ends in the share that holds its last unit:
+            // the largest i with share(i) <= end, that is total i < (end + 1) ctas
             const long long end = item_at + sh.per_item - 1;
-            int c1 = c + 1;
-            while (share(c1 + 1) <= end) ++c1;
-            D.record[2 * c] = make_int4(c1 - c + 1, s.q0, hk, tile);
-            D.record[2 * c + 1] = make_int4(rows, 0, 0, 0);
+            const int parts = whole ? 0 : (int)quotient((end + 1) * ctas - 1, total) - c + 1;
+            const int at = 2 * (D.few ? (b * D.groups + group) * D.tiles_max + tile : c);
+            D.record[at] = make_int4(parts, s.q0, group, tile);
+            D.record[at + 1] = make_int4(rows, c, 0, 0);
         }
         __syncthreads();
         u = item_at + x1;
     }
 }
 
-// grid (shares, R): row r of the item that starts in share c and ends in a
-// later one.  A warp adds up every kJoinWarps-th part, DH / 32 columns a lane.
-constexpr int kJoinWarps = 8;
-template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(DecodeParams D) {
-    constexpr int R = 8 * NT, E = DH / 32;
-    __shared__ float sm_o[kJoinWarps][DH], sm_m[kJoinWarps], sm_l[kJoinWarps];
-    wait_previous();
-    allow_next();
-    const KParams& p = D.p;
-    const int c = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int4 rec = D.record[2 * c];
-    if (rec.x == 0) return;
-    if (r >= D.record[2 * c + 1].x) return;
-    auto slot = [&](int i) { return ((size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R + r); };
-    float M = -FLT_MAX, L = 0.f, O[E];
+// What a join kernel reads of one item: part i of row r of the group's head hx
+// lies in share first + i, in that share's second slot if the item starts there.
+struct Item {
+    int4 a, b;
+    __device__ __forceinline__ int parts() const { return a.x; }
+    __device__ __forceinline__ int rows() const { return b.x; }
+    template <int R>
+    __device__ __forceinline__ size_t at(const DecodeParams& D, int i, int hx, int r) const {
+        return ((size_t)(2 * (b.y + i) + (i == 0 ? 1 : 0)) * D.hc + hx) * R + r;
+    }
+};
+// Parts first, first + step, ... of a packed row, VEC columns a lane.
+template <int DH, int R, int VEC>
+__device__ __forceinline__ void add_parts(const DecodeParams& D, const Item& item, int hx, int r, int first, int step, int lane,
+                                          float& M, float& L, float (&O)[VEC]) {
+    M = -FLT_MAX;
+    L = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) O[e] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < rec.x; i += kJoinWarps) {
-        const float2 ml = *reinterpret_cast<const float2*>(D.part_ml + 2 * slot(i));
-        const float* part = D.part + slot(i) * DH + lane * E;
+    for (int e = 0; e < VEC; ++e) O[e] = 0.f;
+#pragma unroll 8
+    for (int i = first; i < item.parts(); i += step) {
+        const size_t at = item.at<R>(D, i, hx, r);
+        const float2 ml = *reinterpret_cast<const float2*>(D.part_ml + 2 * at);
+        const float* part = D.part + at * DH + lane * VEC;
         const float mn = fmaxf(M, ml.x), old = ex2(M - mn), f = ex2(ml.x - mn);
         M = mn;
         L = L * old + ml.y * f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) O[e] = O[e] * old + part[e] * f;
+        for (int e = 0; e < VEC; ++e) O[e] = O[e] * old + part[e] * f;
     }
+}
+template <bool FP8, int R>
+__device__ __forceinline__ void finish_row(const DecodeParams& D, const Item& item, int hx, int r, int col, float4 O, float M, float L) {
+    const KParams& p = D.p;
+    const int hkv = item.a.z * D.hc + hx, t = (item.a.w * R + r) / p.G, h = hkv * p.G + (item.a.w * R + r) % p.G;
+    put_out(D, item.a.y + t, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
+    if (D.lse && col == 0) D.lse[(long long)(item.a.y + t) * p.Hq + h] = lse_of(M, L);
+}
+
+constexpr int kJoinWarps = 8;
+
+// Few items, each of many parts: grid (items, hc * packed rows), a CTA per row,
+// whose warps add up every kJoinWarps-th part.
+template <int DH, bool FP8, int NT>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid_constant__ DecodeParams D) {
+    constexpr int R = 8 * NT, E = DH / 32;
+    __shared__ __align__(16) float sm_o[kJoinWarps][DH];
+    __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+    wait_previous();
+    allow_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int hx = blockIdx.y % D.hc, r = blockIdx.y / D.hc;
+    const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
+    if (item.parts() == 0 || r >= item.rows()) return;
+    float M, L, O[E];
+    add_parts<DH, R, E>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
 #pragma unroll
     for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = O[e];
     if (lane == 0) {
@@ -602,32 +678,58 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(DecodeParams D) {
         sm_l[warp] = L;
     }
     __syncthreads();
-    const int col = threadIdx.x;
+    const int col = threadIdx.x * 4;
     if (col >= DH) return;
     M = -FLT_MAX;
     L = 0.f;
-    float o = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, sm_m[w]);
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
         const float f = ex2(sm_m[w] - M);
         L += f * sm_l[w];
-        o += f * sm_o[w][col];
+        o = plus(o, *reinterpret_cast<const float4*>(&sm_o[w][col]), f);
     }
-    const int t = (rec.w * R + r) / p.G, h = rec.z * p.G + (rec.w * R + r) % p.G;
-    put_out(D, rec.y + t, h, col, o * ((FP8 ? p.v_scale[rec.z] : 1.f) / L));
-    if (D.lse && col == 0) D.lse[(long long)(rec.y + t) * p.Hq + h] = lse_of(M, L);
+    finish_row<FP8, R>(D, item, hx, r, col, o, M, L);
+}
+
+// Many items, most of two or three parts: grid (shares, hc), the item that
+// starts in share c and ends in a later one, a warp per row.
+template <int DH, bool FP8, int NT>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_shares_kernel(const __grid_constant__ DecodeParams D) {
+    constexpr int R = 8 * NT;
+    wait_previous();
+    allow_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hx = blockIdx.y;
+    const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
+    if (item.parts() == 0) return;
+    for (int r = warp; r < item.rows(); r += kJoinWarps) {
+        float M, L, O[4];
+        const bool on = lane * 4 < DH;
+        add_parts<DH, R, 4>(D, item, hx, r, 0, 1, on ? lane : 0, M, L, O);
+        if (on) finish_row<FP8, R>(D, item, hx, r, lane * 4, make_float4(O[0], O[1], O[2], O[3]), M, L);
+    }
 }
 
 template <int DH, bool FP8, int NT>
-cudaError_t launch(const DecodeParams& D, cudaStream_t s) {
+cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using V = Variant<DH, FP8, NT>;
     static std::atomic<unsigned long long> ready{0};
     cudaError_t e = allow_smem(decode_kernel<DH, FP8, NT>, V::SMEM, ready);
-    if (e == cudaSuccess) e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D);
-    if (e == cudaSuccess) e = launch_early(join_kernel<DH, FP8, NT>, dim3(V::CTAS, V::R), 32 * kJoinWarps, 0, s, D);
-    return e;
+    if (e != cudaSuccess) return e;
+    const int packed = D.p.max_seqlen_q * D.p.G;
+    D.hc = V::RB == 256 || D.p.Hkv % 2 ? 1 : 2;
+    D.groups = D.p.Hkv / D.hc;
+    D.tiles_max = (packed + V::R - 1) / V::R;
+    const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
+    D.few = items <= 64 && D.p.num_seqs <= kThreads;
+    e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D);
+    if (e != cudaSuccess) return e;
+    if (D.few)
+        return launch_early(join_rows_kernel<DH, FP8, NT>, dim3((unsigned)items, D.hc * (packed < V::R ? packed : V::R)),
+                            32 * kJoinWarps, 0, s, D);
+    return launch_early(join_shares_kernel<DH, FP8, NT>, dim3(V::CTAS, D.hc), 32 * kJoinWarps, 0, s, D);
 }
 
 template <int DH, bool FP8>

@@ -104,8 +104,9 @@ struct AppendParams {
 };
 
 // fp2_decode.  p holds what the launch shares with the prefill kernels.
-// Partial results: slot s = one tile's rows [rows][d] fp32 in part, (reference,
-// sum) pairs [rows][2] in part_ml; CTA c of the split owns slots 2c and 2c + 1.
+// Partial results: slot s = one tile's rows of hc heads [hc][rows][d] fp32 in
+// part, (reference, sum) pairs [hc][rows][2] in part_ml; CTA c of the split owns
+// slots 2c and 2c + 1.
 struct DecodeParams {
     KParams p;
     const void *q, *k, *v;
@@ -115,7 +116,11 @@ struct DecodeParams {
     float* part_ml;
     int4* record;              // [kDecCtas][2]: what the join kernel has to do
     float qk_scale;            // log2(e) / sqrt(d)
+    // set by the launcher: KV heads of an item, groups of them, row tiles of the
+    // longest sequence, records by item (few items) or by share
+    int hc, groups, tiles_max, few;
 };
+constexpr int kDecHeads = 2;   // most KV heads of an item
 constexpr int kDecCtas = 444;  // most CTAs of the split: 3 on each of 148 SMs
 constexpr int kDecRows = 32;   // most packed query rows (tokens x group heads) of a tile
 

@@ -58,7 +58,8 @@ struct DecodeLayout {
 };
 DecodeLayout decode_layout(const fp2_params* P) {
     DecodeLayout L;
-    const size_t slots = 2 * (size_t)fp2::kDecCtas * fp2::kDecRows;
+    // (the same for any number of new tokens: a server alternates between them)
+    const size_t slots = 2 * (size_t)fp2::kDecCtas * fp2::kDecHeads * fp2::kDecRows;
     L.part = 256;  // after the error word
     L.part_ml = L.part + slots * P->head_dim * sizeof(float);
     L.record = L.part_ml + slots * 2 * sizeof(float);
