@@ -36,6 +36,7 @@
 //               layout, and at the end normalises O and stores bf16 rows.
 // TMEM: S0 cols [0,128), S1 [128,256), O [256,256+d).
 #include "fp2_attn_common.cuh"
+#include "fp2_launch.cuh"
 
 namespace fp2 {
 
@@ -493,6 +494,17 @@ static bool encode(CUtensorMap* m, bool fp8, int rank, const void* base, const c
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, CUtensorMap* mk,
+                   CUtensorMap* mv) {
+    const bool fp8 = p.fp8 != 0;
+    const cuuint64_t row = (cuuint64_t)p.d * (fp8 ? 1 : 2);
+    cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hkv,
+                          p.paged ? (cuuint64_t)p.num_pages * p.page_size : (cuuint64_t)p.total_k};
+    cuuint64_t str[2] = {row, p.Hkv * row};
+    cuuint32_t box[3] = {fp8 ? 128u : 64u, 1, (cuuint32_t)rows};
+    return encode(mk, fp8, 3, k, dims, str, box) && encode(mv, fp8, 3, v, dims, str, box);
 }
 
 bool make_attn_maps(const KParams& p, const void* q, const void* k, const void* v, int D,

@@ -37,21 +37,27 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = 16;  // keys of a unit: a unit never crosses a page
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
-// A stage of a warp's ring holds the K and V rows of one unit and head.
+// A stage of a warp's ring holds the K and V rows of one unit and head, each as
+// RB / 128 tiles of 16 rows x 128 bytes in the 128-byte swizzle (16-byte chunk c
+// of row r at c ^ (r & 7)), as the tiled copies write them.
 template <int DH, bool FP8, int NT>
 struct Variant {
     static constexpr int R = 8 * NT;
     static constexpr int RB = DH * (FP8 ? 1 : 2);
+    static constexpr int TILE = kUnit * 128;
     static constexpr int STAGE = 2 * kUnit * RB;
     static constexpr int STAGES = RB == 256 ? 3 : NT == 4 ? 5 : 4;
     static constexpr int RING = STAGES * STAGE;             // of one warp
-    static constexpr int SMEM = kWarps * RING;
+    static constexpr bool Q_SMEM = NT == 4;                 // queries: shared memory or registers
+    static constexpr int Q_BYTES = Q_SMEM ? R * DH * 2 : 0; // of one head, as 16-bit values
+    static constexpr int SMEM = kWarps * RING + (RB == 256 ? 1 : kDecHeads) * Q_BYTES;
     static constexpr int PER_SM = RB == 256 || NT > 1 ? 2 : 3;  // CTAs (shared memory and registers)
     static constexpr int CTAS = 148 * PER_SM;
     static constexpr int OS = DH + 4;                       // row stride of the warps' join
     static_assert(R * OS * 4 <= RING, "a warp's partial rows fit its ring");
     static_assert(CTAS <= kDecCtas && R <= kDecRows, "workspace");
 };
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait for a copy
 
 // Weights are taken relative to m = (largest z when m was set) - kLift and may
 // grow to 2^kRoof before m moves: no maximum has to be found in most steps.
@@ -124,18 +130,6 @@ __device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b 
     return make_float4(fmaf(b.x, f, a.x), fmaf(b.y, f, a.y), fmaf(b.z, f, a.z), fmaf(b.w, f, a.w));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 bytes to shared memory, zeros where !on (then nothing is read).
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -165,10 +159,10 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool FP8>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FP8) mma_f16(c, a, b0, b1);
+    else mma_bf16(c, a, b0, b1);
 }
 // Two e4m3 -> two fp16, exact.
 __device__ __forceinline__ uint32_t f16_of(uint32_t x, bool high) {
@@ -185,36 +179,35 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     return d;
 }
 
-// Key of row i of S^T within its unit.  bf16: i.  e4m3: the byte transpose of V
-// puts keys 4 t .. 4 t + 3 into one register, which as 16-bit operands are the
-// product's k = 2 t, 2 t + 1 and 2 t + 8, 2 t + 9; S^T takes its keys in that
-// order, so that no byte of V has to move.
-template <bool FP8>
-__device__ __forceinline__ int key_of(int i) {
-    return FP8 ? 4 * ((i & 7) >> 1) + (i & 1) + 2 * (i >> 3) : i;
-}
-// The 16-byte chunks of a K row are stored at chunk ^ this, of a V row at chunk
-// ^ (row & 7): the 8 rows of a matrix load then lie in different banks.
-template <bool FP8>
-__device__ __forceinline__ int k_swizzle(int row) {
-    return FP8 ? (row & 1) | ((row >> 2) & 3) << 1 : row & 7;
+// e4m3 values enter the products as fp16, converted here (the type's own mma.sync
+// form converts both operands inside, one of them anew for every row tile).
+// A 32-bit register of four e4m3 values gives two 16-bit operand registers, so
+// the products' k runs over the values (first product) or keys (second) in the
+// order 0 1 | 4 5 | 8 9 | 12 13 | 2 3 | 6 7 | 10 11 | 14 15 of each 16.  The queries
+// are laid out in that order; V's rows are loaded so that it comes out natural:
+__device__ __forceinline__ int v_key(int i) {  // row i of the byte transpose
+    return (i & 2) ? 8 + 2 * (i >> 2) + (i & 1) : 2 * (i >> 2) + (i & 1);
 }
 
+struct Maps {
+    CUtensorMap k, v;  // [rows][Hkv][d], boxes of 16 rows x 128 bytes of one head
+};
+
 template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode_kernel(const __grid_constant__ DecodeParams D) {
+__global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
+    decode_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ Maps maps) {
     using V = Variant<DH, FP8, NT>;
     constexpr int R = V::R, RB = V::RB, OS = V::OS, STAGES = V::STAGES;
-    constexpr int CPR = RB / 16;     // 16-byte chunks of a row
-    constexpr int QS = RB / 32;      // k-steps of the first product
+    constexpr int QC = DH / 16;      // k-steps of 16 of the first product
     constexpr int MT = DH / 16;      // row blocks of the second
-    constexpr int LROWS = 32 / CPR;  // rows that a warp copies at once
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ long long sums[kWarps];
-    __shared__ int start_seq;
+    __shared__ int start_seq, aborted;
     __shared__ SeqInfo start_info;
     __shared__ long long start_base, chunk_end;
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
     __shared__ float2 sm_fac[kWarps][STAGES];  // K, V scale factors of the unit in a stage
+    __shared__ __align__(8) uint64_t full[kWarps][STAGES];
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -223,6 +216,16 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
     uint8_t* const my_ring = ring + warp * V::RING;
     const uint32_t my_smem = smem_u32(my_ring);
     const int c = blockIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+        if (warp == 0) {
+            aborted = 0;
+            prefetch_tmap(&maps.k);
+            prefetch_tmap(&maps.v);
+        }
+    }
+    uint32_t phases = 0;  // parity of each stage's next completion
     wait_previous();
     allow_next();
 
@@ -306,72 +309,84 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
         float2 fac_now, fac_next;
         auto load_round = [&](int n0, int& row, float2& fac) {
             const int x = first + (n0 + lane) * kw;
-            const bool on = x < x1 && x * kUnit < seen_any;
+            const bool on = x < x1;
             row = on ? (int)key_row(p, s, b, x * kUnit) : -1;
             fac = make_float2(1.f, 1.f);
             if (FP8 && p.kb_fac && on) {
                 const size_t f = ((size_t)b * p.nkb_max + x * kUnit / p.B) * p.Hkv + hk;
                 fac = make_float2(p.kb_fac[f], p.vb_fac[f]);
+                if (!(fac.x > 0.f && fac.x <= 1.f && fac.y > 0.f && fac.y <= 1.f)) {
+                    set_error(p.err, kErrInvalid, kDetFactor);
+                    fac = make_float2(1.f, 1.f);
+                }
             }
         };
         load_round(0, row_now, fac_now);
         load_round(32, row_next, fac_next);
-        const long long token = (long long)p.Hkv * RB;  // bytes between two tokens' rows
-        const long long lane_at = hk * RB + (lane % CPR) * 16 + (lane / CPR) * token;
-        const uint8_t* const kbase = static_cast<const uint8_t*>(D.k) + lane_at;
-        const long long k_to_v = static_cast<const uint8_t*>(D.v) - static_cast<const uint8_t*>(D.k);
         auto issue = [&](int i, int stage) {
-            if (i < steps) {
-                if (i > 0 && (i & 31) == 0) {
-                    row_now = row_next;
-                    fac_now = fac_next;
-                    load_round(i + 32, row_next, fac_next);
-                }
-                const uint32_t dst = my_smem + stage * V::STAGE + lane / CPR * RB;
-                const int row0 = __shfl_sync(~0u, row_now, i & 31);
-                const int valid = row0 < 0 ? 0 : seen_any - (first + i * kw) * kUnit;
-                if (FP8 && p.kb_fac && lane == (i & 31)) {
-                    if (!(fac_now.x > 0.f && fac_now.x <= 1.f && fac_now.y > 0.f && fac_now.y <= 1.f)) {
-                        set_error(p.err, kErrInvalid, kDetFactor);
-                        fac_now = make_float2(1.f, 1.f);
-                    }
-                    sm_fac[warp][stage] = fac_now;
-                }
-                const uint8_t* from = kbase + max(row0, 0) * token;
+            if (i >= steps) return;
+            if (i > 0 && (i & 31) == 0) {
+                row_now = row_next;
+                fac_now = fac_next;
+                load_round(i + 32, row_next, fac_next);
+            }
+            if (FP8 && p.kb_fac && lane == (i & 31)) sm_fac[warp][stage] = fac_now;
+            const int row0 = __shfl_sync(~0u, row_now, i & 31);
+            if (lane == 0) {
+                uint64_t* bar = &full[warp][stage];
+                const uint32_t dst = my_smem + stage * V::STAGE;
+                if (row0 < 0) {  // a page id out of range, recorded: nothing is read
+                    mbar_arrive(bar);
+                } else {
+                    mbar_arrive_expect_tx(bar, V::STAGE);
 #pragma unroll
-                for (int r0 = 0; r0 < kUnit; r0 += LROWS, from += LROWS * token) {
-                    const int r = r0 + lane / CPR;
-                    const uint32_t kto = dst + r0 * RB + (((lane % CPR) ^ k_swizzle<FP8>(r)) << 4);
-                    const uint32_t vto = dst + r0 * RB + (((lane % CPR) ^ (r & 7)) << 4) + V::STAGE / 2;
-                    if (valid >= kUnit) {
-                        copy16(kto, from);
-                        copy16(vto, from + k_to_v);
-                    } else {
-                        const bool on = r < valid;
-                        const uint8_t* x = on ? from : static_cast<const uint8_t*>(D.k);
-                        copy16(kto, x, on);
-                        copy16(vto, x + k_to_v, on);
+                    for (int h = 0; h < RB / 128; ++h) {
+                        tma_load_3d(dst + h * V::TILE, &maps.k, bar, h * (FP8 ? 128 : 64), hk, row0);
+                        tma_load_3d(dst + V::STAGE / 2 + h * V::TILE, &maps.v, bar, h * (FP8 ? 128 : 64), hk, row0);
                     }
                 }
             }
-            copies_commit();
         };
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
 
         // ---- this warp's query columns, running (m, l, o) ----
-        uint32_t qf[NT][QS][2];
-        float sc[NT][2], m[NT][2], l[NT][2], o[NT][MT][4];
+        // operand registers of 16-value step c of row rq: two pairs of values
+        auto query = [&](int hx, int rq, int ch, int t, uint32_t& b0, uint32_t& b1) {
+            b0 = b1 = 0u;
+            if (rq >= rows) return;
+            const int tok = (tile * R + rq) / p.G, h = (group * D.hc + hx) * p.G + (tile * R + rq) % p.G;
+            const uint8_t* q = static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + tok) * p.Hq + h) * RB;
+            if constexpr (FP8) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(q + 16 * ch + 4 * t);
+                b0 = f16_of(x, false);
+                b1 = f16_of(x, true);
+            } else {
+                b0 = *reinterpret_cast<const uint32_t*>(q + 32 * ch + 4 * t);
+                b1 = *reinterpret_cast<const uint32_t*>(q + 32 * ch + 4 * t + 16);
+            }
+        };
+        uint8_t* const q_smem = ring + kWarps * V::RING;
+        if constexpr (V::Q_SMEM) {
+            // [head][row][2 DH bytes], 16-byte chunk x at x ^ (row & 7) of each 8
+            for (int y = threadIdx.x; y < D.hc * R * QC * 4; y += kThreads) {
+                const int t = y & 3, ch = y / 4 % QC, r = y / 4 / QC % R, hx = y / 4 / QC / R;
+                uint32_t b0, b1;
+                query(hx, r, ch, t, b0, b1);
+                uint8_t* row = q_smem + hx * V::Q_BYTES + r * DH * 2;
+                *reinterpret_cast<uint32_t*>(row + (((2 * ch) ^ (r & 7)) << 4) + 4 * t) = b0;
+                *reinterpret_cast<uint32_t*>(row + (((2 * ch + 1) ^ (r & 7)) << 4) + 4 * t) = b1;
+            }
+            __syncthreads();
+        }
+        uint32_t qf[V::Q_SMEM ? 1 : NT][QC][2];
+        float sc[NT][2], neg_m[NT][2], l[NT][2], o[NT][MT][4];
         int last[NT][2];  // last visible key of rows 2 t4, 2 t4 + 1 of the tile
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int rq = nt * 8 + g;
-            const int tok = (tile * R + rq) / p.G, h = hk * p.G + (tile * R + rq) % p.G;
-            const uint8_t* q = static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + tok) * p.Hq + h) * RB + 4 * t4;
+            if constexpr (!V::Q_SMEM) {
 #pragma unroll
-            for (int ks = 0; ks < QS; ++ks) {
-                qf[nt][ks][0] = rq < rows ? *reinterpret_cast<const uint32_t*>(q + 32 * ks) : 0u;
-                qf[nt][ks][1] = rq < rows ? *reinterpret_cast<const uint32_t*>(q + 32 * ks + 16) : 0u;
+                for (int ch = 0; ch < QC; ++ch) query(hs, nt * 8 + g, ch, t4, qf[nt][ch][0], qf[nt][ch][1]);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -379,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 last[nt][e] = s.P + (tile * R + r) / p.G;
                 sc[nt][e] = D.qk_scale;
                 if constexpr (FP8) sc[nt][e] *= p.q_scale[hk * p.G + (tile * R + r) % p.G] * p.k_scale[hk];
-                m[nt][e] = -FLT_MAX;
+                neg_m[nt][e] = FLT_MAX;
                 l[nt][e] = 0.f;
             }
 #pragma unroll
@@ -387,41 +402,68 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
         }
+        // lane parts of the matrix loads' addresses
+        const uint32_t k_lane = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+        const int v_row = FP8 ? v_key(lane & 15) : (lane & 7) + (lane >> 4) * 8;
+        const uint32_t v_lane = V::STAGE / 2 + v_row * 128 + (((FP8 ? lane >> 4 : (lane >> 3) & 1) ^ (v_row & 7)) << 4);
+        const uint32_t q_lane = smem_u32(q_smem) + hs * V::Q_BYTES + ((lane & 7) + (lane >> 4) * 8) * DH * 2 +
+                                ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 
         int stage = 0, fill = STAGES - 1;
         for (int i = 0; i < steps; ++i) {
-            copies_wait<STAGES - 2>();
+            if (!mbar_wait(&full[warp][stage], (phases >> stage) & 1, &aborted, kWaitNs)) break;
+            phases ^= 1u << stage;
             __syncwarp();
             issue(i + STAGES - 1, fill);
             fill = fill + 1 == STAGES ? 0 : fill + 1;
-            const uint32_t ks0 = my_smem + stage * V::STAGE, vs0 = ks0 + V::STAGE / 2;
+            const uint32_t at0 = my_smem + stage * V::STAGE;
             const int j0 = (first + i * kw) * kUnit;
             float z[NT][4];  // S^T: key g (+ 8 for 2, 3), rows 2 t4, 2 t4 + 1
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
-            {
-                const int r = key_of<FP8>((lane & 7) + ((lane >> 3) & 1) * 8);
+            // one load: 16 keys x 32 bytes, a k-step of bf16 values or two of e4m3
 #pragma unroll
-                for (int ks = 0; ks < QS; ++ks) {
+            for (int ks = 0; ks < RB / 32; ++ks) {
+                uint32_t x[4];
+                ldsm4(x, ((at0 + k_lane) ^ ((ks & 3) << 5)) + (ks >> 2) * V::TILE);
+#pragma unroll
+                for (int half = 0; half < (FP8 ? 2 : 1); ++half) {
+                    const int ch = FP8 ? 2 * ks + half : ks;
                     uint32_t a[4];
-                    ldsm4(a, ks0 + r * RB + (((2 * ks + (lane >> 4)) ^ k_swizzle<FP8>(r)) << 4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if constexpr (FP8) a[e] = f16_of(x[2 * half + (e & 1)], e >= 2);
+                        else a[e] = x[e];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (FP8) mma_e4m3(z[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-                        else mma_bf16(z[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                        if constexpr (!V::Q_SMEM) {
+                            mma16<FP8>(z[nt], a, qf[nt][ch][0], qf[nt][ch][1]);
+                        } else if (nt % 2 == 0) {
+                            uint32_t q[4];
+                            ldsm4(q, (q_lane ^ ((ch & 3) << 5)) + (ch >> 2) * 128 + nt * 8 * DH * 2);
+                            mma16<FP8>(z[nt], a, q[0], q[1]);
+                            mma16<FP8>(z[nt + 1], a, q[2], q[3]);
+                        }
                     }
                 }
             }
             float2 fac = make_float2(1.f, 1.f);
             if (FP8 && p.kb_fac) fac = sm_fac[warp][stage];
+            auto clear = [&](int from) {  // V rows from..15 of the stage
+                for (int y = max(0, from) * 8 + lane; y < kUnit * 8; y += 32)
+#pragma unroll
+                    for (int h = 0; h < RB / 128; ++h)
+                        *reinterpret_cast<uint4*>(my_ring + stage * V::STAGE + V::STAGE / 2 + h * V::TILE + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
+            };
             if (j0 + kUnit > seen_all) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (j0 + key_of<FP8>(g + (e >> 1) * 8) > last[nt][e & 1]) z[nt][e] = -INFINITY;
+                        if (j0 + g + (e >> 1) * 8 > last[nt][e & 1]) z[nt][e] = -INFINITY;
             }
             // exponents of the weights; m moves when one passes the roof
             float w[NT][4], top = -FLT_MAX;
@@ -429,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
             for (int nt = 0; nt < NT; ++nt) {
                 float2 f = make_float2(sc[nt][0], sc[nt][1]);
                 if (FP8 && p.kb_fac) f = make_float2(f.x * fac.x, f.y * fac.x);
-                const float2 shift = make_float2(-m[nt][0], -m[nt][1]);
+                const float2 shift = make_float2(neg_m[nt][0], neg_m[nt][1]);
                 const float2 x = ffma2(make_float2(z[nt][0], z[nt][1]), f, shift), y = ffma2(make_float2(z[nt][2], z[nt][3]), f, shift);
                 w[nt][0] = x.x;
                 w[nt][1] = x.y;
@@ -448,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                         y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
-                        if (y - m[nt][e] > kRoof) {
-                            const float shrink = ex2(m[nt][e] - (y - kLift));
-                            m[nt][e] = y - kLift;
+                        if (y + neg_m[nt][e] > kRoof) {
+                            const float shrink = ex2(kLift - y - neg_m[nt][e]);
+                            neg_m[nt][e] = kLift - y;
                             l[nt][e] *= shrink;
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
@@ -458,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                                 o[nt][mt][e + 2] *= shrink;
                             }
                         }
-                        w[nt][e] = fmaf(z[nt][e], f, -m[nt][e]);
-                        w[nt][e + 2] = fmaf(z[nt][e + 2], f, -m[nt][e]);
+                        w[nt][e] = fmaf(z[nt][e], f, neg_m[nt][e]);
+                        w[nt][e + 2] = fmaf(z[nt][e + 2], f, neg_m[nt][e]);
                     }
             }
             {
@@ -495,15 +537,16 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 uint32_t pair[4];  // e4m3: one load covers two products
                 auto values = [&](int mt, uint32_t (&a)[4]) {  // V^T rows of product mt
                     if constexpr (FP8) {
-                        const int r = lane & 15;
-                        if ((mt & 1) == 0) ldsm_bytes_t(pair, vs0 + r * RB + (((mt + (lane >> 4)) ^ (r & 7)) << 4));
+                        if ((mt & 1) == 0) ldsm_bytes_t(pair, (at0 + v_lane) ^ (mt << 4));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) a[e] = f16_of(pair[2 * (mt & 1) + (e & 1)], e >= 2);
                     } else {
-                        const int r = (lane & 7) + (lane >> 4) * 8;
-                        ldsm4_t(a, vs0 + r * RB + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+                        ldsm4_t(a, ((at0 + v_lane) ^ ((mt & 3) << 5)) + (mt >> 2) * V::TILE);
                     }
                 };
+                // rows of V past the last key that the tile sees: what the cache
+                // holds there is no value of this sequence
+                if (j0 + kUnit > seen_any) clear(seen_any - j0);
                 if (t_first == t_last || j0 + kUnit <= seen_all) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
@@ -525,11 +568,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                     // so token by token, from the last, with the rows it does not
                     // see cleared
                     for (int tok = t_last; tok >= t_first; --tok) {
-                        const int clear = max(0, s.P + tok + 1 - j0);
-                        for (int y = clear * CPR + lane; y < kUnit * CPR; y += 32)
-                            *reinterpret_cast<uint4*>(my_ring + (vs0 - my_smem) + y * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        __syncwarp();
+                        clear(s.P + tok + 1 - j0);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             uint32_t a[4];
@@ -551,10 +590,19 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                         __syncwarp();
                     }
                 }
+                // (generic writes before the next copy into the stage)
+                if (j0 + kUnit > seen_all) fence_proxy_async_smem();
             }
             stage = stage + 1 == STAGES ? 0 : stage + 1;
         }
-        copies_wait<0>();
+        if (*const_cast<volatile int*>(&aborted)) {
+            // a copy did not come: recorded; the others' are waited for and the CTA ends
+            if (lane == 0) set_error(p.err, kErrTimeout, kDetWaitBase);
+            for (int i = 0; i < STAGES; ++i) {
+                int ignore = 0;
+                mbar_wait(&full[warp][i], (phases >> i) & 1, &ignore, kWaitNs / 100);
+            }
+        }
         __syncwarp();
 
         // ---- the warps' parts of this segment, joined in shared memory ----
@@ -569,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 y += __shfl_xor_sync(~0u, y, 16);
                 const int r = nt * 8 + 2 * t4 + e;
                 if (g == 0) {
-                    sm_m[warp][r] = m[nt][e];
+                    sm_m[warp][r] = -neg_m[nt][e];
                     sm_l[warp][r] = y;
                 }
 #pragma unroll
@@ -579,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
                 }
             }
         __syncthreads();
+        if (aborted) return;
         const bool whole = x0 == 0 && x1 == sh.per_item;
         const int slot = 2 * c + (x0 == 0 ? 1 : 0);
         for (int y = threadIdx.x; y < D.hc * rows * (DH / 4); y += kThreads) {
@@ -610,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM) decode
             D.record[at] = make_int4(parts, s.q0, group, tile);
             D.record[at + 1] = make_int4(rows, c, 0, 0);
         }
+        fence_proxy_async_smem();  // the ring held the warps' parts; copies come next
         __syncthreads();
         u = item_at + x1;
     }
@@ -654,7 +704,7 @@ __device__ __forceinline__ void finish_row(const DecodeParams& D, const Item& it
     if (D.lse && col == 0) D.lse[(long long)(item.a.y + t) * p.Hq + h] = lse_of(M, L);
 }
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
 // Few items, each of many parts: grid (items, hc * packed rows), a CTA per row,
 // whose warps add up every kJoinWarps-th part.
@@ -668,6 +718,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hx = blockIdx.y % D.hc, r = blockIdx.y / D.hc;
     const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
+    if (*D.p.err == kErrTimeout) return;  // records may be missing
     if (item.parts() == 0 || r >= item.rows()) return;
     float M, L, O[E];
     add_parts<DH, R, E>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
@@ -696,15 +747,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
 
 // Many items, most of two or three parts: grid (shares, hc), the item that
 // starts in share c and ends in a later one, a warp per row.
+constexpr int kShareWarps = 8;
 template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_shares_kernel(const __grid_constant__ DecodeParams D) {
+__global__ void __launch_bounds__(32 * kShareWarps) join_shares_kernel(const __grid_constant__ DecodeParams D) {
     constexpr int R = 8 * NT;
     wait_previous();
     allow_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hx = blockIdx.y;
     const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
+    if (*D.p.err == kErrTimeout) return;  // records may be missing
     if (item.parts() == 0) return;
-    for (int r = warp; r < item.rows(); r += kJoinWarps) {
+    for (int r = warp; r < item.rows(); r += kShareWarps) {
         float M, L, O[4];
         const bool on = lane * 4 < DH;
         add_parts<DH, R, 4>(D, item, hx, r, 0, 1, on ? lane : 0, M, L, O);
@@ -724,12 +777,14 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
     D.few = items <= 64 && D.p.num_seqs <= kThreads;
-    e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D);
+    Maps maps;
+    if (!make_row_maps(D.p, D.k, D.v, kUnit, &maps.k, &maps.v)) return cudaErrorInvalidValue;
+    e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D, maps);
     if (e != cudaSuccess) return e;
     if (D.few)
         return launch_early(join_rows_kernel<DH, FP8, NT>, dim3((unsigned)items, D.hc * (packed < V::R ? packed : V::R)),
                             32 * kJoinWarps, 0, s, D);
-    return launch_early(join_shares_kernel<DH, FP8, NT>, dim3(V::CTAS, D.hc), 32 * kJoinWarps, 0, s, D);
+    return launch_early(join_shares_kernel<DH, FP8, NT>, dim3(V::CTAS, D.hc), 32 * kShareWarps, 0, s, D);
 }
 
 template <int DH, bool FP8>

@@ -8,18 +8,21 @@
 // start early in turn.  What is saved is the launch latency.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
+
+#include "fp2_internal.h"
 
 namespace fp2 {
 
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-template <typename P>
-inline cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                                const P& params) {
+template <typename... P>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                const P&... params) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -30,12 +33,12 @@ inline cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, params);
+    return cudaLaunchKernelEx(&cfg, kernel, params...);
 }
 
 // Lets `kernel` use `smem` bytes of dynamic shared memory, once per device.
-template <typename P>
-inline cudaError_t allow_smem(void (*kernel)(P), int smem, std::atomic<unsigned long long>& done) {
+template <typename... P>
+inline cudaError_t allow_smem(void (*kernel)(P...), int smem, std::atomic<unsigned long long>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -45,5 +48,9 @@ inline cudaError_t allow_smem(void (*kernel)(P), int smem, std::atomic<unsigned 
     if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
+
+// Tensor maps of the K and V caches as [rows][Hkv][d], whether paged or not, with
+// boxes of `rows` rows x 128 bytes of one head in the 128-byte swizzle (fp2_attn.cu).
+bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, CUtensorMap* mk, CUtensorMap* mv);
 
 }  // namespace fp2
