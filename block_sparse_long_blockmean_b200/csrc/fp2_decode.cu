@@ -227,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     }
     uint32_t phases = 0;  // parity of each stage's next completion
     wait_previous();
-    allow_next();
 
     // total units, this CTA's share of them, and the sequence that holds its first
     SeqInfo s;
@@ -714,7 +713,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     __shared__ __align__(16) float sm_o[kJoinWarps][DH];
     __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
     wait_previous();
-    allow_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hx = blockIdx.y % D.hc, r = blockIdx.y / D.hc;
     const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
@@ -752,7 +750,6 @@ template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kShareWarps) join_shares_kernel(const __grid_constant__ DecodeParams D) {
     constexpr int R = 8 * NT;
     wait_previous();
-    allow_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hx = blockIdx.y;
     const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
     if (*D.p.err == kErrTimeout) return;  // records may be missing
