@@ -2,150 +2,206 @@
 // and the write of q and of the cache rows of k and v, one pass over the
 // projection's rows.
 //
+// Mathematics: with r = 1 / sqrt(mean(x^2) + eps) and the norm's weight w, every
+// stored value is r (x_i C_i + x_j S_i), j its partner in the rotated pair:
+// C = w cos, S = -+ w_j sin.  C and S are the same for all heads of a token, so a
+// warp takes them once and then streams heads: two packed products a pair, the
+// square sum over the head's lanes, one rounding.
+//
 // A head of a token is held by D / 8 lanes with 8 values each, as two groups
-// of 4 that rotate with each other: values a..a+3 and b..b+3 with b = a +
-// rot/2 for the half-split pairing, so that no value crosses lanes; only the
-// mean square of a norm is summed over the head's lanes.
+// of 4, values a..a+3 and b..b+3 with b = a + rot/2, so that a half-split pair
+// (i, i + rot/2) and an adjacent pair (2i, 2i + 1) both stay inside a lane.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "fp2_device.cuh"
-#include "fp2_internal.h"
+#include "fp2_launch.cuh"
 
 namespace fp2 {
 
 namespace {
 
-constexpr int kAppThreads = 256;
+constexpr int kAppThreads = 128, kAppWarps = kAppThreads / 32;
+constexpr int kAppDepth = 4;  // groups of heads whose rows a warp loads at once
 
-__device__ __forceinline__ void load4(const void* base, long long at, float* x) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
-    x[0] = __uint_as_float(w.x << 16);
-    x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(w.y << 16);
-    x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+struct Quad {
+    float2 x, y;
+};
+__device__ __forceinline__ Quad unpack(uint2 w) {
+    return {make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u)),
+            make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u))};
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 swapped(float2 a) { return make_float2(a.y, a.x); }
 
-// The one rounding: to bf16, or to e4m3 of x * (1 / scale).  The product
-// with the reciprocal is off by under 2^-22 relative, far below e4m3's 2^-4.
+// The one rounding: to bf16, or to e4m3 (the caller has divided by the scale).
 template <bool FP8>
-__device__ __forceinline__ void store4(void* base, long long at, const float* x, float inv_scale) {
+__device__ __forceinline__ void store4(void* base, long long at, Quad v) {
     if constexpr (FP8) {
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(base) + at) =
-            pack_e4m3x4(x[0] * inv_scale, x[1] * inv_scale, x[2] * inv_scale, x[3] * inv_scale);
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(base) + at) = pack_e4m3x4(v.x.x, v.x.y, v.y.x, v.y.y);
     } else {
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) =
-            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+            make_uint2(pack_bf16x2(v.x.x, v.x.y), pack_bf16x2(v.y.x, v.y.y));
     }
 }
 
-// grid (ceil(T / warps), head chunks): a warp takes one token and a chunk of
-// its Hq + 2 Hkv heads, 32 / (D / 8) heads at a time.
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kAppThreads) append_kernel(AppendParams p, int chunk) {
+// grid (ceil(T / warps), chunks): a warp takes one token and a chunk of its
+// groups of 32 / (D / 8) heads (q's, then k's, then v's).
+template <int D, bool FP8, bool ADJACENT>
+__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int HL = D / 8, HPW = 32 / HL;
     const int lane = threadIdx.x & 31, l = lane % HL;
-    const int tok = blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5);
+    const int tok = blockIdx.x * kAppWarps + (threadIdx.x >> 5);
+    wait_previous();
     if (tok >= p.total_q) return;
-    const int heads = p.Hq + 2 * p.Hkv, rot = p.rot;
+    const int rot = p.rot;
     const bool rotates = l < rot / 8;
     // this lane's two groups of four values
     const int ia = rotates ? 4 * l : rot + 4 * (l - rot / 8);
     const int ib = rotates ? rot / 2 + 4 * l : ia + (D - rot) / 2;
-    float cs[4], sn[4];
+    int slot = p.slots[tok];
+    Quad ca = {{1.f, 1.f}, {1.f, 1.f}}, cb = ca, sa = {{0.f, 0.f}, {0.f, 0.f}}, sb = sa;  // cos, -+ sin
     if (rotates) {
         const double pos = (double)p.positions[tok];
+        float c[4], s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // pair (a[e], b[e]) of the half-split form turns with frequency
-            // 4l + e; the interleaved pairs sit inside the groups
-            const int f = !p.interleaved ? 4 * l + e : (e < 2 ? ia / 2 + e : ib / 2 + e - 2);
+            // pair (a[e], b[e]) turns with frequency 4 l + e; adjacent pairs sit
+            // inside the groups
+            const int f = !ADJACENT ? 4 * l + e : (e < 2 ? ia / 2 + e : ib / 2 + e - 2);
             // turns = position * frequency / 2 pi in 64 bits (a float holds no
             // far position's angle), of which only the fraction matters
             const double turns = pos * (double)p.inv_freq[f] * 0.15915494309189533577;
-            float s, c;
-            sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-            cs[e] = c * p.rope_scale;
-            sn[e] = s * p.rope_scale;
+            sincospif(2.0f * (float)(turns - rint(turns)), &s[e], &c[e]);
+            c[e] *= p.rope_scale;
+            s[e] *= p.rope_scale;
+        }
+        if constexpr (!ADJACENT) {
+            ca = cb = {{c[0], c[1]}, {c[2], c[3]}};
+            sb = {{s[0], s[1]}, {s[2], s[3]}};
+            sa = {{-s[0], -s[1]}, {-s[2], -s[3]}};
+        } else {
+            ca = {{c[0], c[0]}, {c[1], c[1]}};
+            cb = {{c[2], c[2]}, {c[3], c[3]}};
+            sa = {{-s[0], s[0]}, {-s[1], s[1]}};
+            sb = {{-s[2], s[2]}, {-s[3], s[3]}};
         }
     }
-    int slot = p.slots[tok];
     if (slot >= p.cache_rows) {
         if (lane == 0 && blockIdx.y == 0) set_error(p.err, kErrBounds, kDetRow);
         slot = -1;
     }
-    const int h_end = min(heads, (int)(blockIdx.y + 1) * chunk);
-    for (int h0 = blockIdx.y * chunk; h0 < h_end; h0 += HPW) {
-        const int hh = h0 + lane / HL;
-        const bool on = hh < h_end;
-        const int kind = hh < p.Hq ? 0 : hh < p.Hq + p.Hkv ? 1 : 2;  // q, k, v
-        const int h = kind == 0 ? hh : kind == 1 ? hh - p.Hq : hh - p.Hq - p.Hkv;
-        float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-        if (on) {
-            const void* src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-            const long long row = (long long)tok * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + h * D;
-            load4(src, row + ia, a);
-            load4(src, row + ib, b);
-        }
-        const float* w = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ss += a[e] * a[e] + b[e] * b[e];
-#pragma unroll
-        for (int o = HL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        if (!on) continue;
-        if (w) {
-            const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                a[e] = a[e] * r * w[ia + e];
-                b[e] = b[e] * r * w[ib + e];
-            }
-        }
-        if (kind < 2 && rotates) {
-            if (!p.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = a[e], y = b[e];
-                    a[e] = x * cs[e] - y * sn[e];
-                    b[e] = y * cs[e] + x * sn[e];
-                }
+
+    const int nq = (p.Hq + HPW - 1) / HPW, nk = (p.Hkv + HPW - 1) / HPW;
+    const int g0 = blockIdx.y * p.chunk, g1 = min(g0 + p.chunk, nq + 2 * nk);
+    // groups [from, to) of one kind; TURN: norm and rotation, else as they are
+    auto stream = [&](auto turn, int from, int to, const void* src, long long stride, void* dst, long long row, int heads,
+                      const float* weight, const float* scale) {
+        constexpr bool TURN = decltype(turn)::value;
+        if (from >= to) return;
+        const uint16_t* in = static_cast<const uint16_t*>(src) + (long long)tok * stride;
+        const long long out = row * heads * D;
+        Quad wca = ca, wcb = cb, wsa = sa, wsb = sb;
+        if (TURN && weight) {
+            const float4 x = *reinterpret_cast<const float4*>(weight + ia), y = *reinterpret_cast<const float4*>(weight + ib);
+            const Quad wa = {{x.x, x.y}, {x.z, x.w}}, wb = {{y.x, y.y}, {y.z, y.w}};
+            wca = {mul2(ca.x, wa.x), mul2(ca.y, wa.y)};
+            wcb = {mul2(cb.x, wb.x), mul2(cb.y, wb.y)};
+            if constexpr (!ADJACENT) {
+                wsa = {mul2(sa.x, wb.x), mul2(sa.y, wb.y)};
+                wsb = {mul2(sb.x, wa.x), mul2(sb.y, wa.y)};
             } else {
+                wsa = {mul2(sa.x, swapped(wa.x)), mul2(sa.y, swapped(wa.y))};
+                wsb = {mul2(sb.x, swapped(wb.x)), mul2(sb.y, swapped(wb.y))};
+            }
+        }
+        for (int g = from; g < to; g += kAppDepth) {
+            uint2 raw[kAppDepth][2];
+            float inv[kAppDepth];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = a[2 * e], y = a[2 * e + 1];
-                    a[2 * e] = x * cs[e] - y * sn[e];
-                    a[2 * e + 1] = y * cs[e] + x * sn[e];
-                    x = b[2 * e];
-                    y = b[2 * e + 1];
-                    b[2 * e] = x * cs[2 + e] - y * sn[2 + e];
-                    b[2 * e + 1] = y * cs[2 + e] + x * sn[2 + e];
+            for (int i = 0; i < kAppDepth; ++i) {
+                const int h = (g + i) * HPW + lane / HL;
+                raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+                inv[i] = 1.f;
+                if (g + i < to && h < heads) {
+                    raw[i][0] = *reinterpret_cast<const uint2*>(in + h * D + ia);
+                    raw[i][1] = *reinterpret_cast<const uint2*>(in + h * D + ib);
+                    if constexpr (FP8) inv[i] = scale[h];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAppDepth; ++i) {
+                if (g + i >= to) break;
+                const int h = (g + i) * HPW + lane / HL;
+                Quad a = unpack(raw[i][0]), b = unpack(raw[i][1]);
+                // (the reciprocal is off by 2^-23 of its value, far below e4m3's 2^-4)
+                float r = FP8 ? __fdividef(1.f, inv[i]) : 1.f;
+                if constexpr (TURN) {
+                    if (weight) {
+                        float2 q = ffma2(a.y, a.y, mul2(a.x, a.x));
+                        q = ffma2(b.y, b.y, ffma2(b.x, b.x, q));
+                        float ss = q.x + q.y;
+#pragma unroll
+                        for (int o = HL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                        r *= rsqrtf(ss * (1.0f / D) + p.eps);
+                    }
+                    Quad x = {mul2(a.x, wca.x), mul2(a.y, wca.y)}, y = {mul2(b.x, wcb.x), mul2(b.y, wcb.y)};
+                    if (rotates) {
+                        if constexpr (!ADJACENT) {
+                            x = {ffma2(b.x, wsa.x, x.x), ffma2(b.y, wsa.y, x.y)};
+                            y = {ffma2(a.x, wsb.x, y.x), ffma2(a.y, wsb.y, y.y)};
+                        } else {
+                            x = {ffma2(swapped(a.x), wsa.x, x.x), ffma2(swapped(a.y), wsa.y, x.y)};
+                            y = {ffma2(swapped(b.x), wsb.x, y.x), ffma2(swapped(b.y), wsb.y, y.y)};
+                        }
+                    }
+                    a = x;
+                    b = y;
+                }
+                if (TURN || FP8) {
+                    const float2 rr = make_float2(r, r);
+                    a = {mul2(a.x, rr), mul2(a.y, rr)};
+                    b = {mul2(b.x, rr), mul2(b.y, rr)};
+                }
+                if (h < heads && row >= 0) {
+                    store4<FP8>(dst, out + h * D + ia, a);
+                    store4<FP8>(dst, out + h * D + ib, b);
                 }
             }
         }
-        if (kind != 0 && slot < 0) continue;
-        void* dst = kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache;
-        const long long at = kind == 0 ? ((long long)tok * p.Hq + h) * D : ((long long)slot * p.Hkv + h) * D;
-        const float inv = FP8 ? 1.0f / (kind == 0 ? p.q_scale : kind == 1 ? p.k_scale : p.v_scale)[h] : 1.0f;
-        store4<FP8>(dst, at + ia, a, inv);
-        store4<FP8>(dst, at + ib, b, inv);
-    }
+    };
+    stream(std::true_type{}, g0, min(g1, nq), p.q, p.q_stride, p.q_out, tok, p.Hq, p.q_weight, p.q_scale);
+    stream(std::true_type{}, max(g0, nq) - nq, min(g1, nq + nk) - nq, p.k, p.k_stride, p.k_cache, slot, p.Hkv, p.k_weight, p.k_scale);
+    stream(std::false_type{}, max(g0, nq + nk) - nq - nk, g1 - nq - nk, p.v, p.v_stride, p.v_cache, slot, p.Hkv, nullptr, p.v_scale);
+}
+
+template <int D, bool FP8>
+cudaError_t launch(AppendParams p, cudaStream_t s) {
+    constexpr int HPW = 32 / (D / 8);
+    const int groups = (p.Hq + HPW - 1) / HPW + 2 * ((p.Hkv + HPW - 1) / HPW);
+    // all heads of a token in one warp once the tokens alone fill the machine
+    // (16 warps on each of 148 SMs), fewer and fewer below that
+    long long chunk = ((long long)p.total_q * groups + 148 * 16 - 1) / (148 * 16);
+    p.chunk = (int)(chunk < groups ? chunk : groups);
+    const dim3 grid((p.total_q + kAppWarps - 1) / kAppWarps, (groups + p.chunk - 1) / p.chunk);
+    return p.interleaved ? launch_early(append_kernel<D, FP8, true>, grid, kAppThreads, 0, s, p)
+                         : launch_early(append_kernel<D, FP8, false>, grid, kAppThreads, 0, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
-    const int heads = p.Hq + 2 * p.Hkv, hpw = 32 / (p.d / 8);
-    const int warps = kAppThreads / 32;
-    const dim3 grid((p.total_q + warps - 1) / warps, 1);
-    const int chunk = (heads + hpw - 1) / hpw * hpw;
-    if (p.d == 128) {
-        if (p.fp8) append_kernel<128, true><<<grid, kAppThreads, 0, s>>>(p, chunk);
-        else append_kernel<128, false><<<grid, kAppThreads, 0, s>>>(p, chunk);
-    } else {
-        if (p.fp8) append_kernel<64, true><<<grid, kAppThreads, 0, s>>>(p, chunk);
-        else append_kernel<64, false><<<grid, kAppThreads, 0, s>>>(p, chunk);
-    }
-    return cudaGetLastError();
+    if (p.d == 128) return p.fp8 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+    return p.fp8 ? launch<64, true>(p, s) : launch<64, false>(p, s);
 }
 
 }  // namespace fp2

@@ -100,6 +100,7 @@ struct AppendParams {
     const float *q_scale, *k_scale, *v_scale;
     float eps, rope_scale;
     int total_q, Hq, Hkv, d, rot, interleaved, cache_rows, fp8;
+    int chunk;                 // set by the launcher: groups of heads per warp
     uint32_t* err;
 };
 

@@ -7,7 +7,7 @@
 // memory (they are a few KB and come from L2), and then maps its share of the
 // tokens and pages by binary search, so that no CTA waits for another.
 #include "fp2_device.cuh"
-#include "fp2_internal.h"
+#include "fp2_launch.cuh"
 
 namespace fp2 {
 
@@ -58,7 +58,7 @@ __device__ __forceinline__ int owner(const int* v, int n, int i) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kMapThreads) page_map_kernel(MapParams p) {
+__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const __grid_constant__ MapParams p) {
     extern __shared__ int map_smem[];
     __shared__ longlong2 warp_sums[kMapThreads / 32];
     __shared__ int bad_len, bad_pages;
@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(MapParams p) {
     int* cu = map_smem;          // [S + 1] exclusive sums of new tokens
     int* pc = map_smem + S + 1;  // [S + 1] exclusive sums of new pages
     if (threadIdx.x == 0) bad_len = bad_pages = 0;
+    wait_previous();
     __syncthreads();
     // a thread takes `per` consecutive sequences
     const int per = (S + kMapThreads - 1) / kMapThreads;
@@ -166,16 +167,15 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(MapParams p) {
 cudaError_t launch_page_map(const MapParams& p, cudaStream_t s) {
     const size_t smem = 2 * ((size_t)p.num_seqs + 1) * sizeof(int);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<unsigned long long> ready{0};
+        const cudaError_t e = allow_smem(page_map_kernel, 2 * (16384 + 1) * (int)sizeof(int), ready);
         if (e != cudaSuccess) return e;
     }
     const int tokens_per_cta = 4 * kMapThreads;
     int ctas = (p.total_q + tokens_per_cta - 1) / tokens_per_cta;
     if (ctas < 1) ctas = 1;
     if (ctas > 296) ctas = 296;
-    page_map_kernel<<<ctas, kMapThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(page_map_kernel, dim3(ctas), kMapThreads, smem, s, p);
 }
 
 }  // namespace fp2

@@ -156,7 +156,9 @@ fp2_status fp2_append(const fp2_append_io* io, fp2_dtype dtype, const fp2_params
         io->k_stride % 4 || io->v_stride % 4)
         return FP2_ERR_INVALID_ARG;
     if (!aligned(io->q, 8) || !aligned(io->k, 8) || !aligned(io->v, 8) || !aligned(io->q_out, 16) ||
-        !aligned(io->k_cache, 16) || !aligned(io->v_cache, 16))
+        !aligned(io->k_cache, 16) || !aligned(io->v_cache, 16) || !aligned(io->q_weight, 16) ||
+        !aligned(io->k_weight, 16) || !aligned(io->inv_freq, 4) || !aligned(io->positions, 4) ||
+        !aligned(io->slot_map, 4))
         return FP2_ERR_INVALID_ARG;
     // extents, for the overlap checks: the strided rows' hull and the outputs
     const size_t T = (size_t)P->total_q, elt = fp8 ? 1 : 2;
@@ -171,7 +173,7 @@ fp2_status fp2_append(const fp2_append_io* io, fp2_dtype dtype, const fp2_params
     for (const void* c : {(const void*)io->k_cache, (const void*)io->v_cache})
         if (overlap(c, nc, io->q, nq) || overlap(c, nc, io->k, nk) || overlap(c, nc, io->v, nv))
             return FP2_ERR_INVALID_ARG;
-    fp2::AppendParams a;
+    fp2::AppendParams a = {};
     a.q = io->q;
     a.k = io->k;
     a.v = io->v;

@@ -374,7 +374,7 @@ typedef struct fp2_append_io {
  * outside the cache other than a negative one records FP2_ERR_DEVICE_BOUNDS
  * (detail 7) and is not written; of two tokens with one slot either may win.
  * q_out may be q itself when q is bf16 rows without a gap; the other buffers
- * must not overlap.  Base pointers are 8-byte aligned, outputs 16.
+ * must not overlap.  q, k and v are 8-byte aligned, weights and outputs 16.
  * Caches quantised per key block (params->k_block_factor) are not written by
  * this call: FP2_ERR_UNSUPPORTED.  Reads params: heads, head_dim, total_q,
  * total_k or page_size and num_pages, scales, workspace, stream. */

@@ -111,7 +111,8 @@ def test_append_refuses_sizes(lib, field, value, code):
     ("eps", float("nan"), INVALID), ("eps", float("inf"), INVALID), ("rope_scale", float("nan"), INVALID), ("interleaved", 2, INVALID),
     ("inv_freq", None, INVALID), ("positions", None, INVALID), ("slot_map", None, INVALID), ("q", None, INVALID), ("k", None, INVALID),
     ("v", None, INVALID), ("q_out", None, INVALID), ("k_cache", None, INVALID), ("v_cache", None, INVALID), ("q_stride", 1020, INVALID),
-    ("k_stride", 252, INVALID), ("v_stride", 257, INVALID), ("q", (1 << 32) + 4, INVALID), ("q_out", (9 << 32) + 8, INVALID),
+    ("k_stride", 252, INVALID), ("v_stride", 257, INVALID), ("q", (1 << 32) + 4, INVALID), ("q_weight", (4 << 32) + 8, INVALID), ("k_weight", (5 << 32) + 4, INVALID),
+    ("inv_freq", (6 << 32) + 2, INVALID), ("positions", (7 << 32) + 1, INVALID), ("slot_map", (8 << 32) + 2, INVALID), ("q_out", (9 << 32) + 8, INVALID),
     ("k_cache", (10 << 32) + 8, INVALID), ("k_cache", 11 << 32, INVALID), ("v_cache", (1 << 32) + 1024, INVALID), ("q_out", 1 << 32, INVALID)])
 def test_append_refuses_io(lib, field, value, code):
     assert call_append(lib, append_io(**{field: value}), params()) == code
