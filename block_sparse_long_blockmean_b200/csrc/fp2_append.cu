@@ -45,19 +45,18 @@ __device__ __forceinline__ float2 swapped(float2 a) { return make_float2(a.y, a.
 
 // The one rounding: to bf16, or to e4m3 (the caller has divided by the scale).
 template <bool FP8>
-__device__ __forceinline__ void store4(void* base, long long at, Quad v) {
+__device__ __forceinline__ void store4(uint8_t* to, Quad v) {
     if constexpr (FP8) {
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(base) + at) = pack_e4m3x4(v.x.x, v.x.y, v.y.x, v.y.y);
+        *reinterpret_cast<uint32_t*>(to) = pack_e4m3x4(v.x.x, v.x.y, v.y.x, v.y.y);
     } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) =
-            make_uint2(pack_bf16x2(v.x.x, v.x.y), pack_bf16x2(v.y.x, v.y.y));
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x.x, v.x.y), pack_bf16x2(v.y.x, v.y.y));
     }
 }
 
 // grid (ceil(T / warps), chunks): a warp takes one token and a chunk of its
 // groups of 32 / (D / 8) heads (q's, then k's, then v's).
 template <int D, bool FP8, bool ADJACENT>
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int HL = D / 8, HPW = 32 / HL;
     const int lane = threadIdx.x & 31, l = lane % HL;
     const int tok = blockIdx.x * kAppWarps + (threadIdx.x >> 5);
@@ -124,29 +123,37 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
                 wsb = {mul2(sb.x, swapped(wb.x)), mul2(sb.y, swapped(wb.y))};
             }
         }
-        for (int g = from; g < to; g += kAppDepth) {
+        const bool norm = TURN && weight;
+        // this lane's first values of the present step; a group is GS values on
+        constexpr int GS = HPW * D, ES = FP8 ? 1 : 2;
+        const uint16_t* ra = in + (from * HPW + lane / HL) * D + ia;
+        const uint16_t* rb = ra + (ib - ia);
+        uint8_t* wa = static_cast<uint8_t*>(dst) + (out + (from * HPW + lane / HL) * D + ia) * ES;
+        uint8_t* wb = wa + (ib - ia) * ES;
+        [[maybe_unused]] const float* sp = FP8 ? scale + from * HPW + lane / HL : nullptr;
+        auto step = [&](auto full, int g) {
+            constexpr bool FULL = decltype(full)::value;  // kAppDepth whole groups
             uint2 raw[kAppDepth][2];
             float inv[kAppDepth];
+            auto on = [&](int i) { return FULL || (g + i < to && (g + i) * HPW + lane / HL < heads); };
 #pragma unroll
             for (int i = 0; i < kAppDepth; ++i) {
-                const int h = (g + i) * HPW + lane / HL;
                 raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
                 inv[i] = 1.f;
-                if (g + i < to && h < heads) {
-                    raw[i][0] = *reinterpret_cast<const uint2*>(in + h * D + ia);
-                    raw[i][1] = *reinterpret_cast<const uint2*>(in + h * D + ib);
-                    if constexpr (FP8) inv[i] = scale[h];
+                if (on(i)) {
+                    raw[i][0] = *reinterpret_cast<const uint2*>(ra + i * GS);
+                    raw[i][1] = *reinterpret_cast<const uint2*>(rb + i * GS);
+                    if constexpr (FP8) inv[i] = sp[i * HPW];
                 }
             }
 #pragma unroll
             for (int i = 0; i < kAppDepth; ++i) {
-                if (g + i >= to) break;
-                const int h = (g + i) * HPW + lane / HL;
+                if (!FULL && g + i >= to) break;
                 Quad a = unpack(raw[i][0]), b = unpack(raw[i][1]);
                 // (the reciprocal is off by 2^-23 of its value, far below e4m3's 2^-4)
                 float r = FP8 ? __fdividef(1.f, inv[i]) : 1.f;
                 if constexpr (TURN) {
-                    if (weight) {
+                    if (norm) {
                         float2 q = ffma2(a.y, a.y, mul2(a.x, a.x));
                         q = ffma2(b.y, b.y, ffma2(b.x, b.x, q));
                         float ss = q.x + q.y;
@@ -172,12 +179,21 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
                     a = {mul2(a.x, rr), mul2(a.y, rr)};
                     b = {mul2(b.x, rr), mul2(b.y, rr)};
                 }
-                if (h < heads && row >= 0) {
-                    store4<FP8>(dst, out + h * D + ia, a);
-                    store4<FP8>(dst, out + h * D + ib, b);
+                if (on(i) && row >= 0) {
+                    store4<FP8>(wa + i * GS * ES, a);
+                    store4<FP8>(wb + i * GS * ES, b);
                 }
             }
-        }
+            ra += kAppDepth * GS;
+            rb += kAppDepth * GS;
+            wa += kAppDepth * GS * ES;
+            wb += kAppDepth * GS * ES;
+            if constexpr (FP8) sp += kAppDepth * HPW;
+        };
+        int g = from;
+        if (heads % HPW == 0)
+            for (; g + kAppDepth <= to; g += kAppDepth) step(std::true_type{}, g);
+        for (; g < to; g += kAppDepth) step(std::false_type{}, g);
     };
     stream(std::true_type{}, g0, min(g1, nq), p.q, p.q_stride, p.q_out, tok, p.Hq, p.q_weight, p.q_scale);
     stream(std::true_type{}, max(g0, nq) - nq, min(g1, nq + nk) - nq, p.k, p.k_stride, p.k_cache, slot, p.Hkv, p.k_weight, p.k_scale);

@@ -58,13 +58,16 @@ __device__ __forceinline__ int owner(const int* v, int n, int i) {
     return lo;
 }
 
+// TOKENS consecutive tokens a thread.
+template <int TOKENS>
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const __grid_constant__ MapParams p) {
     extern __shared__ int map_smem[];
     __shared__ longlong2 warp_sums[kMapThreads / 32];
     __shared__ int bad_len, bad_pages;
     const int S = p.num_seqs;
     int* cu = map_smem;          // [S + 1] exclusive sums of new tokens
-    int* pc = map_smem + S + 1;  // [S + 1] exclusive sums of new pages
+    int* pc = cu + S + 1;        // [S + 1] exclusive sums of new pages
+    int* had = pc + S + 1;       // [S] tokens that were there
     if (threadIdx.x == 0) bad_len = bad_pages = 0;
     wait_previous();
     __syncthreads();
@@ -103,6 +106,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const __grid_cons
             read(b, pre, n);
             cu[b] = (int)nt;
             pc[b] = (int)np;
+            had[b] = pre;
             nt += n;
             np += pages(pre + n) - pages(pre);
         }
@@ -126,56 +130,75 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const __grid_cons
     }
     const int live = ok ? (int)all_t : 0, fresh = ok ? (int)all_p : 0;
     const int first = blockIdx.x * kMapThreads + threadIdx.x, step = gridDim.x * kMapThreads;
-    auto free_page = [&](int j) {  // page j of the step's new ones, -1 if its id is bad
-        const int id = p.free_pages[head + j];
+    auto checked = [&](int id) {  // a page id, -1 if it is bad
         if (id < 0 || id >= p.num_pages) {
             set_error(p.err, kErrBounds, kDetPage);
             return -1;
         }
         return id;
     };
+    // tokens, TOKENS consecutive ones a thread: one search, then a walk
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
+    for (long long i0 = (long long)first * TOKENS; i0 < p.total_q; i0 += (long long)step * TOKENS) {
+        int pos[TOKENS], slot[TOKENS], id[TOKENS];
+        int b = i0 < live ? owner(cu, S, (int)i0) : S - 1;
+#pragma unroll
+        for (int e = 0; e < TOKENS; ++e) {
+            const int i = (int)i0 + e;
+            pos[e] = 0;
+            id[e] = -1;
+            if (i < live) {
+                while (i >= cu[b + 1]) ++b;
+                pos[e] = had[b] + (i - cu[b]);
+                const int k = pos[e] >> p.page_shift, old = pages(had[b]);
+                // the prefix's last page, not full, or one of the step's new ones
+                id[e] = k < old ? p.table[(size_t)b * p.max_pages + k] : p.free_pages[head + pc[b] + (k - old)];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < TOKENS; ++e) {
+            slot[e] = -1;
+            if (i0 + e < live && checked(id[e]) >= 0) slot[e] = (id[e] << p.page_shift) + (pos[e] & (p.page_size - 1));
+        }
+        if (TOKENS == 4 && wide && i0 + 4 <= p.total_q) {
+            *reinterpret_cast<int4*>(p.positions + i0) = make_int4(pos[0], pos[1 % TOKENS], pos[2 % TOKENS], pos[3 % TOKENS]);
+            *reinterpret_cast<int4*>(p.slots + i0) = make_int4(slot[0], slot[1 % TOKENS], slot[2 % TOKENS], slot[3 % TOKENS]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < TOKENS; ++e)
+                if (i0 + e < p.total_q) {
+                    p.positions[i0 + e] = pos[e];
+                    p.slots[i0 + e] = slot[e];
+                }
+        }
+    }
     for (int j = first; j < fresh; j += step) {
         const int b = owner(pc, S, j);
-        p.table[(size_t)b * p.max_pages + pages(p.prefix[b]) + (j - pc[b])] = free_page(j);
-    }
-    for (int i = first; i < p.total_q; i += step) {
-        int pos = 0, slot = -1;
-        if (i < live) {
-            const int b = owner(cu, S, i);
-            const int pre = p.prefix[b];
-            pos = pre + (i - cu[b]);
-            const int k = pos >> p.page_shift, old = pages(pre);
-            int id;
-            if (k < old) {  // the prefix's last page, not full
-                id = p.table[(size_t)b * p.max_pages + k];
-                if (id < 0 || id >= p.num_pages) {
-                    set_error(p.err, kErrBounds, kDetPage);
-                    id = -1;
-                }
-            } else {
-                id = free_page(pc[b] + (k - old));
-            }
-            if (id >= 0) slot = (id << p.page_shift) + (pos & (p.page_size - 1));
-        }
-        p.positions[i] = pos;
-        p.slots[i] = slot;
+        p.table[(size_t)b * p.max_pages + pages(had[b]) + (j - pc[b])] = checked(p.free_pages[head + j]);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_page_map(const MapParams& p, cudaStream_t s) {
-    const size_t smem = 2 * ((size_t)p.num_seqs + 1) * sizeof(int);
+template <int TOKENS>
+static cudaError_t launch(const MapParams& p, cudaStream_t s) {
+    const size_t smem = (3 * (size_t)p.num_seqs + 2) * sizeof(int);
     if (smem > 40 * 1024) {
         static std::atomic<unsigned long long> ready{0};
-        const cudaError_t e = allow_smem(page_map_kernel, 2 * (16384 + 1) * (int)sizeof(int), ready);
+        const cudaError_t e = allow_smem(page_map_kernel<TOKENS>, (3 * 16384 + 2) * (int)sizeof(int), ready);
         if (e != cudaSuccess) return e;
     }
-    const int tokens_per_cta = 4 * kMapThreads;
-    int ctas = (p.total_q + tokens_per_cta - 1) / tokens_per_cta;
-    if (ctas < 1) ctas = 1;
-    if (ctas > 296) ctas = 296;
-    return launch_early(page_map_kernel, dim3(ctas), kMapThreads, smem, s, p);
+    const int per_cta = TOKENS * kMapThreads;
+    int ctas = (p.total_q + per_cta - 1) / per_cta;
+    ctas = ctas < 1 ? 1 : ctas > 296 ? 296 : ctas;
+    return launch_early(page_map_kernel<TOKENS>, dim3(ctas), kMapThreads, smem, s, p);
+}
+
+cudaError_t launch_page_map(const MapParams& p, cudaStream_t s) {
+    // a token a thread while that takes at most one CTA on each of 148 SMs
+    // (64 single tokens: 2.8 us, with four a thread 3.7); more tokens share their
+    // CTA's sums and searches (254K tokens of 1000 sequences: 7.3 and 5.3 us)
+    return p.total_q <= 148 * kMapThreads ? launch<1>(p, s) : launch<4>(p, s);
 }
 
 }  // namespace fp2
