@@ -675,24 +675,53 @@ struct Item {
         return ((size_t)(2 * (b.y + i) + (i == 0 ? 1 : 0)) * D.hc + hx) * R + r;
     }
 };
-// Parts first, first + step, ... of a packed row, VEC columns a lane.
-template <int DH, int R, int VEC>
+// Parts first, first + step, ... of a packed row, VEC columns a lane; BATCH of
+// them are loaded at once, so that their latencies overlap.
+template <int DH, int R, int VEC, int BATCH>
 __device__ __forceinline__ void add_parts(const DecodeParams& D, const Item& item, int hx, int r, int first, int step, int lane,
                                           float& M, float& L, float (&O)[VEC]) {
     M = -FLT_MAX;
     L = 0.f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) O[e] = 0.f;
-#pragma unroll 8
-    for (int i = first; i < item.parts(); i += step) {
-        const size_t at = item.at<R>(D, i, hx, r);
-        const float2 ml = *reinterpret_cast<const float2*>(D.part_ml + 2 * at);
-        const float* part = D.part + at * DH + lane * VEC;
-        const float mn = fmaxf(M, ml.x), old = ex2(M - mn), f = ex2(ml.x - mn);
-        M = mn;
-        L = L * old + ml.y * f;
+    for (int i0 = first; i0 < item.parts(); i0 += BATCH * step) {
+        float2 ml[BATCH];
+        float part[BATCH][VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) O[e] = O[e] * old + part[e] * f;
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k * step;
+            const bool on = i < item.parts();
+            const size_t at = item.at<R>(D, on ? i : first, hx, r);
+            ml[k] = *reinterpret_cast<const float2*>(D.part_ml + 2 * at);
+            if constexpr (VEC == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(D.part + at * DH + lane * VEC);
+                part[k][0] = x.x;
+                part[k][1] = x.y;
+                part[k][2] = x.z;
+                part[k][3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(D.part + at * DH + lane * VEC);
+                part[k][0] = x.x;
+                part[k][1] = x.y;
+            }
+            if (!on) ml[k] = make_float2(-INFINITY, 0.f);
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) mn = fmaxf(mn, ml[k].x);
+        const float old = ex2(M - mn);
+        M = mn;
+        L *= old;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) O[e] *= old;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            if (i0 + k * step >= item.parts()) break;
+            const float f = ex2(ml[k].x - mn);
+            L += ml[k].y * f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) O[e] += part[k][e] * f;
+        }
     }
 }
 template <bool FP8, int R>
@@ -719,7 +748,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     if (*D.p.err == kErrTimeout) return;  // records may be missing
     if (item.parts() == 0 || r >= item.rows()) return;
     float M, L, O[E];
-    add_parts<DH, R, E>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
+    add_parts<DH, R, E, 8>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
 #pragma unroll
     for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = O[e];
     if (lane == 0) {
@@ -757,7 +786,7 @@ __global__ void __launch_bounds__(32 * kShareWarps) join_shares_kernel(const __g
     for (int r = warp; r < item.rows(); r += kShareWarps) {
         float M, L, O[4];
         const bool on = lane * 4 < DH;
-        add_parts<DH, R, 4>(D, item, hx, r, 0, 1, on ? lane : 0, M, L, O);
+        add_parts<DH, R, 4, 4>(D, item, hx, r, 0, 1, on ? lane : 0, M, L, O);
         if (on) finish_row<FP8, R>(D, item, hx, r, lane * 4, make_float4(O[0], O[1], O[2], O[3]), M, L);
     }
 }
