@@ -50,7 +50,10 @@ struct Variant {
     static constexpr int RING = STAGES * STAGE;             // of one warp
     static constexpr bool Q_SMEM = NT == 4;                 // queries: shared memory or registers
     static constexpr int Q_BYTES = Q_SMEM ? R * DH * 2 : 0; // of one head, as 16-bit values
-    static constexpr int SMEM = kWarps * RING + (RB == 256 ? 1 : kDecHeads) * Q_BYTES;
+    // two adjacent KV heads an item where two CTAs still fit an SM: a token's rows
+    // of both are one piece of 256 or 512 bytes for the DRAM
+    static constexpr int HEADS = RB == 256 && Q_SMEM ? 1 : kDecHeads;
+    static constexpr int SMEM = kWarps * RING + HEADS * Q_BYTES;
     static constexpr int PER_SM = RB == 256 || NT > 1 ? 2 : 3;  // CTAs (shared memory and registers)
     static constexpr int CTAS = 148 * PER_SM;
     static constexpr int OS = DH + 4;                       // row stride of the warps' join
@@ -691,20 +694,25 @@ __device__ __forceinline__ void add_parts(const DecodeParams& D, const Item& ite
         for (int k = 0; k < BATCH; ++k) {
             const int i = i0 + k * step;
             const bool on = i < item.parts();
-            const size_t at = item.at<R>(D, on ? i : first, hx, r);
-            ml[k] = *reinterpret_cast<const float2*>(D.part_ml + 2 * at);
-            if constexpr (VEC == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(D.part + at * DH + lane * VEC);
-                part[k][0] = x.x;
-                part[k][1] = x.y;
-                part[k][2] = x.z;
-                part[k][3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(D.part + at * DH + lane * VEC);
-                part[k][0] = x.x;
-                part[k][1] = x.y;
+            const size_t at = item.at<R>(D, i, hx, r);
+            ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) part[k][e] = 0.f;
+            if (on) {
+                ml[k] = *reinterpret_cast<const float2*>(D.part_ml + 2 * at);
+                const float* from = D.part + at * DH + lane * VEC;
+                if constexpr (VEC == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(from);
+                    part[k][0] = x.x;
+                    part[k][1] = x.y;
+                    part[k][2] = x.z;
+                    part[k][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(from);
+                    part[k][0] = x.x;
+                    part[k][1] = x.y;
+                }
             }
-            if (!on) ml[k] = make_float2(-INFINITY, 0.f);
         }
         float mn = M;
 #pragma unroll
@@ -716,7 +724,6 @@ __device__ __forceinline__ void add_parts(const DecodeParams& D, const Item& ite
         for (int e = 0; e < VEC; ++e) O[e] *= old;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            if (i0 + k * step >= item.parts()) break;
             const float f = ex2(ml[k].x - mn);
             L += ml[k].y * f;
 #pragma unroll
@@ -798,13 +805,15 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     cudaError_t e = allow_smem(decode_kernel<DH, FP8, NT>, V::SMEM, ready);
     if (e != cudaSuccess) return e;
     const int packed = D.p.max_seqlen_q * D.p.G;
-    D.hc = V::RB == 256 || D.p.Hkv % 2 ? 1 : 2;
+    D.hc = D.p.Hkv % V::HEADS ? 1 : V::HEADS;
     D.groups = D.p.Hkv / D.hc;
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
     D.few = items <= 64 && D.p.num_seqs <= kThreads;
     Maps maps;
-    if (!make_row_maps(D.p, D.k, D.v, kUnit, &maps.k, &maps.v)) return cudaErrorInvalidValue;
+    // L2 fetches in pieces of 256 bytes where the item reads both halves
+    const bool wide = D.hc * V::RB >= 256 || D.p.Hkv == 1;
+    if (!make_row_maps(D.p, D.k, D.v, kUnit, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
     e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D, maps);
     if (e != cudaSuccess) return e;
     if (D.few)

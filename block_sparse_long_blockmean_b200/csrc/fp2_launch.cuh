@@ -50,7 +50,8 @@ inline cudaError_t allow_smem(void (*kernel)(P...), int smem, std::atomic<unsign
 }
 
 // Tensor maps of the K and V caches as [rows][Hkv][d], whether paged or not, with
-// boxes of `rows` rows x 128 bytes of one head in the 128-byte swizzle (fp2_attn.cu).
-bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, CUtensorMap* mk, CUtensorMap* mv);
+// boxes of `rows` rows x 128 bytes of one head in the 128-byte swizzle; L2 fetches
+// them in pieces of 256 (wide) or 128 bytes (fp2_attn.cu).
+bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, bool wide, CUtensorMap* mk, CUtensorMap* mv);
 
 }  // namespace fp2
