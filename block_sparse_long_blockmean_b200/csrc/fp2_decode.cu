@@ -24,17 +24,15 @@
 // 8 rows; it is bound by the cache's bytes, not by these products.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <float.h>
 
-#include "fp2_launch.cuh"
-#include "fp2_seq.cuh"
+#include "fp2_decode.cuh"
 
 namespace fp2 {
 
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kUnit = 16;  // keys of a unit: a unit never crosses a page
+constexpr int kUnit = kDecBox;  // keys of a unit: one copy
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
 // A stage of a warp's ring holds the K and V rows of one unit and head, each as
@@ -60,79 +58,6 @@ struct Variant {
     static_assert(R * OS * 4 <= RING, "a warp's partial rows fit its ring");
     static_assert(CTAS <= kDecCtas && R <= kDecRows, "workspace");
 };
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait for a copy
-
-// Weights are taken relative to m = (largest z when m was set) - kLift and may
-// grow to 2^kRoof before m moves: no maximum has to be found in most steps.
-// fp16 weights then span 2^kRoof (its largest is just under 2^16) down to
-// 2^-24, that is 2^-31 of the row's largest.
-constexpr float kLift = 7.f, kRoof = 15.f;
-
-struct Shape {
-    long long units;  // of the sequence
-    int per_item;     // units of one item: ceil(Lk / kUnit)
-    int tiles;        // row tiles per head group
-};
-template <int R>
-__device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const SeqInfo& s) {
-    Shape x;
-    x.per_item = (s.Lk + kUnit - 1) / kUnit;
-    x.tiles = (s.Lq * D.p.G + R - 1) / R;
-    x.units = (long long)x.per_item * x.tiles * D.groups;
-    return x;
-}
-// Sequence b's lengths and its units; 0 units if it rests or its lengths are bad.
-template <int R>
-__device__ __forceinline__ long long seq_units(const DecodeParams& D, int b, SeqInfo& s) {
-    if (!load_seq(D.p, b, s) || s.Lq == 0) return 0;
-    return seq_shape<R>(D, s).units;
-}
-// a / b of values that mostly fit 32 bits.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
-}
-
-// Sum of x over the CTA and the exclusive prefix of the calling thread.
-__device__ __forceinline__ long long block_prefix(long long x, long long& total, long long* sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long y = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(~0u, y, o);
-        if (lane >= o) y += u;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = y;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    return before + y - x;
-}
-
-// Four columns of one packed row's output, rounded once.
-__device__ __forceinline__ void put_out(const DecodeParams& D, long long row, int h, int col, float4 x) {
-    const KParams& p = D.p;
-    const long long at = (row * p.Hq + h) * p.d + col;
-    if (p.out_fp8) {
-        const float sc = p.out_scale ? p.out_scale[h] : p.v_scale[h / p.G];
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D.out) + at) = pack_e4m3x4(x.x / sc, x.y / sc, x.z / sc, x.w / sc);
-    } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(D.out) + at) =
-            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-    }
-}
-__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
-__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
-__device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b f
-    return make_float4(fmaf(b.x, f, a.x), fmaf(b.y, f, a.y), fmaf(b.z, f, a.z), fmaf(b.w, f, a.w));
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -192,22 +117,15 @@ __device__ __forceinline__ int v_key(int i) {  // row i of the byte transpose
     return (i & 2) ? 8 + 2 * (i >> 2) + (i & 1) : 2 * (i >> 2) + (i & 1);
 }
 
-struct Maps {
-    CUtensorMap k, v;  // [rows][Hkv][d], boxes of 16 rows x 128 bytes of one head
-};
-
 template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
-    decode_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ Maps maps) {
+    decode_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ DecodeMaps maps) {
     using V = Variant<DH, FP8, NT>;
     constexpr int R = V::R, RB = V::RB, OS = V::OS, STAGES = V::STAGES;
     constexpr int QC = DH / 16;      // k-steps of 16 of the first product
     constexpr int MT = DH / 16;      // row blocks of the second
     extern __shared__ __align__(1024) uint8_t ring[];
-    __shared__ long long sums[kWarps];
-    __shared__ int start_seq, aborted;
-    __shared__ SeqInfo start_info;
-    __shared__ long long start_base, chunk_end;
+    __shared__ int aborted;
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
     __shared__ float2 sm_fac[kWarps][STAGES];  // K, V scale factors of the unit in a stage
     __shared__ __align__(8) uint64_t full[kWarps][STAGES];
@@ -231,76 +149,15 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     uint32_t phases = 0;  // parity of each stage's next completion
     wait_previous();
 
-    // total units, this CTA's share of them, and the sequence that holds its first
-    SeqInfo s;
-    long long total = 0, n = threadIdx.x < p.num_seqs ? seq_units<R>(D, threadIdx.x, s) : 0;
-    long long at = block_prefix(n, total, sums);
-    for (int b0 = kThreads; b0 < p.num_seqs; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        long long t;
-        SeqInfo x;
-        block_prefix(b < p.num_seqs ? seq_units<R>(D, b, x) : 0, t, sums);
-        total += t;
-    }
-    if (!D.few) {
-        if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
-    } else if (c == 0 && threadIdx.x < p.num_seqs) {
-        // (few: a record per item, at most as many sequences as threads; the
-        // tiles that this sequence does not have)
-        const int tiles = n > 0 ? seq_shape<R>(D, s).tiles : 0;
-        for (int i = 0; i < D.groups; ++i)
-            for (int j = tiles; j < D.tiles_max; ++j)
-                D.record[2 * ((threadIdx.x * D.groups + i) * D.tiles_max + j)] = make_int4(0, 0, 0, 0);
-    }
-    // a share is at least one unit of each warp
-    const long long want = (total + kw - 1) / kw;
-    const int ctas = (int)(want < gridDim.x ? (want > 0 ? want : 1) : gridDim.x);
-    if (c >= ctas || total == 0) return;
-    auto share = [&](int i) { return quotient(total * i, ctas); };
-    long long u = share(c);
-    const long long u_end = share(c + 1);
-    for (int b0 = 0;;) {
-        if (n > 0 && at <= u && u < at + n) {
-            start_seq = b0 + threadIdx.x;
-            start_base = at;
-            start_info = s;
-        }
-        if ((b0 += kThreads) >= p.num_seqs) break;
-        const int b = b0 + threadIdx.x;
-        // (the next chunk's sequences start where this chunk's end)
-        if (threadIdx.x == kThreads - 1) chunk_end = at + n;
-        __syncthreads();
-        const long long base = chunk_end;
-        long long t;
-        n = b < p.num_seqs ? seq_units<R>(D, b, s) : 0;
-        at = base + block_prefix(n, t, sums);
-    }
-    __syncthreads();
-    int b = start_seq;
-    long long seq_at = start_base;
-    s = start_info;
-
-    while (u < u_end) {
-        Shape sh = seq_shape<R>(D, s);
-        while (u >= seq_at + sh.units) {  // on to the sequence that holds u
-            seq_at += sh.units;
-            do
-                if (++b >= p.num_seqs) return;
-            while (!load_seq(p, b, s) || s.Lq == 0);
-            sh = seq_shape<R>(D, s);
-        }
-        const int item = (int)quotient(u - seq_at, sh.per_item);
-        const long long item_at = seq_at + (long long)item * sh.per_item;
-        const int group = item / sh.tiles, tile = item % sh.tiles;
+    Share share;  // a share is at least one unit of each warp
+    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.x, kw, share)) return;
+    const SeqInfo& s = share.s;
+    Segment seg;
+    while (next_segment<R, kUnit>(D, share, seg)) {
+        const int b = share.b, group = seg.group, tile = seg.tile, rows = seg.rows;
         const int hk = group * D.hc + hs;
-        const int x0 = (int)(u - item_at);
-        const int x1 = (int)min((long long)sh.per_item, u_end - item_at);
-
-        // packed rows of the tile: row r is token (tile * R + r) / G, head r % G
-        const int rows = min(R, s.Lq * p.G - tile * R);
-        const int t_first = tile * R / p.G, t_last = (tile * R + rows - 1) / p.G;
-        const int seen_all = s.P + t_first + 1;  // keys that every row of the tile sees
-        const int seen_any = s.P + t_last + 1;   // keys past it are not read
+        const int x0 = seg.x0, x1 = seg.x1, t_first = seg.t_first, t_last = seg.t_last;
+        const int seen_all = seg.seen_all, seen_any = seg.seen_any;
 
         // ---- the copies of this warp: its units are kw apart ----
         const int first = x0 + warp / D.hc;
@@ -413,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
 
         int stage = 0, fill = STAGES - 1;
         for (int i = 0; i < steps; ++i) {
-            if (!mbar_wait(&full[warp][stage], (phases >> stage) & 1, &aborted, kWaitNs)) break;
+            if (!mbar_wait(&full[warp][stage], (phases >> stage) & 1, &aborted, kDecWaitNs)) break;
             phases ^= 1u << stage;
             __syncwarp();
             issue(i + STAGES - 1, fill);
@@ -602,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
             if (lane == 0) set_error(p.err, kErrTimeout, kDetWaitBase);
             for (int i = 0; i < STAGES; ++i) {
                 int ignore = 0;
-                mbar_wait(&full[warp][i], (phases >> i) & 1, &ignore, kWaitNs / 100);
+                mbar_wait(&full[warp][i], (phases >> i) & 1, &ignore, kDecWaitNs / 100);
             }
         }
         __syncwarp();
@@ -630,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
             }
         __syncthreads();
         if (aborted) return;
-        const bool whole = x0 == 0 && x1 == sh.per_item;
+        const bool whole = seg.whole();
         const int slot = 2 * c + (x0 == 0 ? 1 : 0);
         for (int y = threadIdx.x; y < D.hc * rows * (DH / 4); y += kThreads) {
             const int col = y % (DH / 4) * 4, r = y / (DH / 4) % rows, hx = y / (DH / 4) / rows;
@@ -652,18 +509,10 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(M, L);
             }
         }
-        if (threadIdx.x == 0 && x0 == 0 && (D.few || !whole)) {
-            // an item that goes on ends in the share that holds its last unit:
-            // the largest i with share(i) <= end, that is total i < (end + 1) ctas
-            const long long end = item_at + sh.per_item - 1;
-            const int parts = whole ? 0 : (int)quotient((end + 1) * ctas - 1, total) - c + 1;
-            const int at = 2 * (D.few ? (b * D.groups + group) * D.tiles_max + tile : c);
-            D.record[at] = make_int4(parts, s.q0, group, tile);
-            D.record[at + 1] = make_int4(rows, c, 0, 0);
-        }
+        if (threadIdx.x == 0) put_record(D, share, seg, c);
         fence_proxy_async_smem();  // the ring held the warps' parts; copies come next
         __syncthreads();
-        u = item_at + x1;
+        share.u = seg.item_at + x1;
     }
 }
 
@@ -810,7 +659,7 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
     D.few = items <= 64 && D.p.num_seqs <= kThreads;
-    Maps maps;
+    DecodeMaps maps;
     // L2 fetches in pieces of 256 bytes where the item reads both halves
     const bool wide = D.hc * V::RB >= 256 || D.p.Hkv == 1;
     if (!make_row_maps(D.p, D.k, D.v, kUnit, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;

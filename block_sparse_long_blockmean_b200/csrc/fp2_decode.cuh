@@ -1,0 +1,210 @@
+// fp2_decode.cuh -- what the two decode kernels share: the split of the keys
+// into shares, the output of a row, the records for the join.
+#pragma once
+
+#include <float.h>
+
+#include "fp2_launch.cuh"
+#include "fp2_seq.cuh"
+
+namespace fp2 {
+
+constexpr uint64_t kDecWaitNs = 2000000000ull;  // 2 s per wait for a copy or a product
+constexpr int kDecBox = 16;                     // rows of a copy: they never cross a page
+
+// Weights are taken relative to m = (largest z when m was set) - kLift and may
+// grow to 2^kRoof before m moves: no maximum has to be found in most steps.
+// fp16 weights then span 2^kRoof (its largest is just under 2^16) down to
+// 2^-24, that is 2^-31 of the row's largest.
+constexpr float kLift = 7.f, kRoof = 15.f;
+
+struct DecodeMaps {
+    CUtensorMap k, v;  // [rows][Hkv][d], boxes of kDecBox rows x 128 bytes of one head
+};
+
+struct Shape {
+    long long units;  // of the sequence
+    int per_item;     // units of one item: ceil(Lk / UNIT)
+    int tiles;        // row tiles per head group
+};
+template <int R, int UNIT>
+__device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const SeqInfo& s) {
+    Shape x;
+    x.per_item = (s.Lk + UNIT - 1) / UNIT;
+    x.tiles = (s.Lq * D.p.G + R - 1) / R;
+    x.units = (long long)x.per_item * x.tiles * D.groups;
+    return x;
+}
+// Sequence b's lengths and its units; 0 units if it rests or its lengths are bad.
+template <int R, int UNIT>
+__device__ __forceinline__ long long seq_units(const DecodeParams& D, int b, SeqInfo& s) {
+    if (!load_seq(D.p, b, s) || s.Lq == 0) return 0;
+    return seq_shape<R, UNIT>(D, s).units;
+}
+// a / b of values that mostly fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
+// Sum of x over the CTA of W warps and the exclusive prefix of the calling thread.
+template <int W>
+__device__ __forceinline__ long long block_prefix(long long x, long long& total, long long* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(~0u, y, o);
+        if (lane >= o) y += u;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = y;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    return before + y - x;
+}
+
+// Share c of `shares` at most: units [u, u_end) of `total` cut into `parts` equal
+// shares, starting in sequence b, whose units start at seq_at and whose lengths
+// are s.  False (for the whole CTA) if the share is empty.  A share has at least
+// `least` units.  Also clears the records that nobody else will write.
+struct Share {
+    long long total, u, u_end, seq_at;
+    int parts, b;
+    SeqInfo s;
+    __device__ __forceinline__ long long start(int i) const { return quotient(total * i, parts); }
+    // the last share that an item reaches whose last unit is `end`: the largest i
+    // with start(i) <= end, that is total i < (end + 1) parts
+    __device__ __forceinline__ int of_unit(long long end) const { return (int)quotient((end + 1) * parts - 1, total); }
+};
+template <int R, int UNIT, int W>
+__device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int shares, int least, Share& x) {
+    __shared__ long long sums[W];
+    __shared__ Share found;
+    __shared__ long long chunk_end;
+    const KParams& p = D.p;
+    constexpr int T = 32 * W;
+    SeqInfo s;
+    long long total = 0, n = (int)threadIdx.x < p.num_seqs ? seq_units<R, UNIT>(D, threadIdx.x, s) : 0;
+    long long at = block_prefix<W>(n, total, sums);
+    for (int b0 = T; b0 < p.num_seqs; b0 += T) {
+        const int b = b0 + threadIdx.x;
+        long long t;
+        SeqInfo y;
+        block_prefix<W>(b < p.num_seqs ? seq_units<R, UNIT>(D, b, y) : 0, t, sums);
+        total += t;
+    }
+    if (!D.few) {
+        if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
+    } else if (c == 0 && (int)threadIdx.x < p.num_seqs) {
+        // (few: a record per item, at most as many sequences as threads; the
+        // tiles that this sequence does not have)
+        const int tiles = n > 0 ? seq_shape<R, UNIT>(D, s).tiles : 0;
+        for (int i = 0; i < D.groups; ++i)
+            for (int j = tiles; j < D.tiles_max; ++j)
+                D.record[2 * ((threadIdx.x * D.groups + i) * D.tiles_max + j)] = make_int4(0, 0, 0, 0);
+    }
+    const long long want = (total + least - 1) / least;
+    x.total = total;
+    x.parts = (int)(want < shares ? (want > 0 ? want : 1) : shares);
+    if (c >= x.parts || total == 0) return false;
+    x.u = x.start(c);
+    x.u_end = x.start(c + 1);
+    for (int b0 = 0;;) {
+        if (n > 0 && at <= x.u && x.u < at + n) {
+            found.b = b0 + threadIdx.x;
+            found.seq_at = at;
+            found.s = s;
+        }
+        if ((b0 += T) >= p.num_seqs) break;
+        const int b = b0 + threadIdx.x;
+        // (the next chunk's sequences start where this chunk's end)
+        if (threadIdx.x == T - 1) chunk_end = at + n;
+        __syncthreads();
+        const long long base = chunk_end;
+        long long t;
+        n = b < p.num_seqs ? seq_units<R, UNIT>(D, b, s) : 0;
+        at = base + block_prefix<W>(n, t, sums);
+    }
+    __syncthreads();
+    x.b = found.b;
+    x.seq_at = found.seq_at;
+    x.s = found.s;
+    return true;
+}
+
+// A segment: units [x0, x1) of one item, the part of it that lies in the share.
+struct Segment {
+    long long item_at;
+    int per_item, group, tile, x0, x1;
+    int rows, t_first, t_last;  // packed rows of the tile and the tokens they span
+    int seen_all, seen_any;     // keys that every row sees, that some row sees
+    __device__ __forceinline__ bool whole() const { return x0 == 0 && x1 == per_item; }
+};
+// The segment that starts at unit x.u; false at the share's end.
+template <int R, int UNIT>
+__device__ __forceinline__ bool next_segment(const DecodeParams& D, Share& x, Segment& g) {
+    if (x.u >= x.u_end) return false;
+    const KParams& p = D.p;
+    Shape sh = seq_shape<R, UNIT>(D, x.s);
+    while (x.u >= x.seq_at + sh.units) {  // on to the sequence that holds u
+        x.seq_at += sh.units;
+        do
+            if (++x.b >= p.num_seqs) return false;
+        while (!load_seq(p, x.b, x.s) || x.s.Lq == 0);
+        sh = seq_shape<R, UNIT>(D, x.s);
+    }
+    const int item = (int)quotient(x.u - x.seq_at, sh.per_item);
+    g.item_at = x.seq_at + (long long)item * sh.per_item;
+    g.per_item = sh.per_item;
+    g.group = item / sh.tiles;
+    g.tile = item % sh.tiles;
+    g.x0 = (int)(x.u - g.item_at);
+    g.x1 = (int)min((long long)sh.per_item, x.u_end - g.item_at);
+    // packed row r is token (tile * R + r) / G, head r % G of the group
+    g.rows = min(R, x.s.Lq * p.G - g.tile * R);
+    g.t_first = g.tile * R / p.G;
+    g.t_last = (g.tile * R + g.rows - 1) / p.G;
+    g.seen_all = x.s.P + g.t_first + 1;
+    g.seen_any = x.s.P + g.t_last + 1;
+    return true;
+}
+// One thread: what the join has to do for an item that starts in this segment.
+__device__ __forceinline__ void put_record(const DecodeParams& D, const Share& x, const Segment& g, int c) {
+    if (g.x0 != 0 || !(D.few || !g.whole())) return;
+    const int parts = g.whole() ? 0 : x.of_unit(g.item_at + g.per_item - 1) - c + 1;
+    const int at = 2 * (D.few ? (x.b * D.groups + g.group) * D.tiles_max + g.tile : c);
+    D.record[at] = make_int4(parts, x.s.q0, g.group, g.tile);
+    D.record[at + 1] = make_int4(g.rows, c, 0, 0);
+}
+
+// Four columns of one packed row's output, rounded once.
+__device__ __forceinline__ void put_out(const DecodeParams& D, long long row, int h, int col, float4 x) {
+    const KParams& p = D.p;
+    const long long at = (row * p.Hq + h) * p.d + col;
+    if (p.out_fp8) {
+        const float sc = p.out_scale ? p.out_scale[h] : p.v_scale[h / p.G];
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D.out) + at) = pack_e4m3x4(x.x / sc, x.y / sc, x.z / sc, x.w / sc);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(D.out) + at) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
+__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+__device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b f
+    return make_float4(fmaf(b.x, f, a.x), fmaf(b.y, f, a.y), fmaf(b.z, f, a.z), fmaf(b.w, f, a.w));
+}
+
+// Multi-token tiles of head dimension 128 (fp2_decode_tiles.cu): the shares'
+// partial rows and records, as decode_kernel leaves them for 32 rows a tile.
+cudaError_t launch_decode_tiles(const DecodeParams& D, int shares, cudaStream_t s);
+int decode_tile_shares(const DecodeParams& D);
+
+}  // namespace fp2
