@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     wait_previous();
 
     Share share;  // a share is at least one unit of each warp
-    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.x, kw, share)) return;
+    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.x, kw, true, share)) return;
     const SeqInfo& s = share.s;
     Segment seg;
     while (next_segment<R, kUnit>(D, share, seg)) {
@@ -650,25 +650,35 @@ __global__ void __launch_bounds__(32 * kShareWarps) join_shares_kernel(const __g
 template <int DH, bool FP8, int NT>
 cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using V = Variant<DH, FP8, NT>;
-    static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = allow_smem(decode_kernel<DH, FP8, NT>, V::SMEM, ready);
-    if (e != cudaSuccess) return e;
+    // more than 8 packed rows at head dimension 128: whole tiles on the tensor core
+    constexpr bool TILES = DH == 128 && NT == 4;
     const int packed = D.p.max_seqlen_q * D.p.G;
-    D.hc = D.p.Hkv % V::HEADS ? 1 : V::HEADS;
+    D.hc = D.p.Hkv % (TILES ? 2 : V::HEADS) ? 1 : TILES ? 2 : V::HEADS;
     D.groups = D.p.Hkv / D.hc;
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
     D.few = items <= 64 && D.p.num_seqs <= kThreads;
-    DecodeMaps maps;
-    // L2 fetches in pieces of 256 bytes where the item reads both halves
-    const bool wide = D.hc * V::RB >= 256 || D.p.Hkv == 1;
-    if (!make_row_maps(D.p, D.k, D.v, kUnit, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
-    e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D, maps);
+    int shares;
+    cudaError_t e;
+    if constexpr (TILES) {
+        shares = decode_tile_shares(D);
+        e = launch_decode_tiles(D, s);
+    } else {
+        shares = V::CTAS;
+        static std::atomic<unsigned long long> ready{0};
+        e = allow_smem(decode_kernel<DH, FP8, NT>, V::SMEM, ready);
+        if (e != cudaSuccess) return e;
+        DecodeMaps maps;
+        // L2 fetches in pieces of 256 bytes where the item reads both halves
+        const bool wide = D.hc * V::RB >= 256 || D.p.Hkv == 1;
+        if (!make_row_maps(D.p, D.k, D.v, kUnit, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
+        e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D, maps);
+    }
     if (e != cudaSuccess) return e;
     if (D.few)
         return launch_early(join_rows_kernel<DH, FP8, NT>, dim3((unsigned)items, D.hc * (packed < V::R ? packed : V::R)),
                             32 * kJoinWarps, 0, s, D);
-    return launch_early(join_shares_kernel<DH, FP8, NT>, dim3(V::CTAS, D.hc), 32 * kShareWarps, 0, s, D);
+    return launch_early(join_shares_kernel<DH, FP8, NT>, dim3(shares, D.hc), 32 * kShareWarps, 0, s, D);
 }
 
 template <int DH, bool FP8>

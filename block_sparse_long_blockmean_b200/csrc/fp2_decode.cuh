@@ -73,7 +73,7 @@ __device__ __forceinline__ long long block_prefix(long long x, long long& total,
 // Share c of `shares` at most: units [u, u_end) of `total` cut into `parts` equal
 // shares, starting in sequence b, whose units start at seq_at and whose lengths
 // are s.  False (for the whole CTA) if the share is empty.  A share has at least
-// `least` units.  Also clears the records that nobody else will write.
+// `least` units.  With `records` also clears those that nobody else will write.
 struct Share {
     long long total, u, u_end, seq_at;
     int parts, b;
@@ -84,7 +84,7 @@ struct Share {
     __device__ __forceinline__ int of_unit(long long end) const { return (int)quotient((end + 1) * parts - 1, total); }
 };
 template <int R, int UNIT, int W>
-__device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int shares, int least, Share& x) {
+__device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int shares, int least, bool records, Share& x) {
     __shared__ long long sums[W];
     __shared__ Share found;
     __shared__ long long chunk_end;
@@ -100,7 +100,8 @@ __device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int sha
         block_prefix<W>(b < p.num_seqs ? seq_units<R, UNIT>(D, b, y) : 0, t, sums);
         total += t;
     }
-    if (!D.few) {
+    if (!records) {
+    } else if (!D.few) {
         if (threadIdx.x == 0) D.record[2 * c] = make_int4(0, 0, 0, 0);
     } else if (c == 0 && (int)threadIdx.x < p.num_seqs) {
         // (few: a record per item, at most as many sequences as threads; the
@@ -204,7 +205,7 @@ __device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b 
 
 // Multi-token tiles of head dimension 128 (fp2_decode_tiles.cu): the shares'
 // partial rows and records, as decode_kernel leaves them for 32 rows a tile.
-cudaError_t launch_decode_tiles(const DecodeParams& D, int shares, cudaStream_t s);
+cudaError_t launch_decode_tiles(const DecodeParams& D, cudaStream_t s);
 int decode_tile_shares(const DecodeParams& D);
 
 }  // namespace fp2

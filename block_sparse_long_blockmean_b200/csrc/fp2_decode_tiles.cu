@@ -1,0 +1,546 @@
+// fp2_decode_tiles.cu -- fp2_decode for several new tokens a sequence (drafts that
+// are checked at once): tiles of 128 keys against up to 32 packed query rows on
+// the 5th-generation tensor core, head dimension 128.
+//
+// Mathematics as in fp2_decode.cu, with the keys as the product's 128 rows:
+//   S^T (128 keys x 32 rows)  = K (128 x d) Q^T           both K-major
+//   O^T (128 d x 32 rows)    += V^T (d x 128 keys) P^T    both MN-major, as stored
+// so that neither K nor V is transposed or converted; a thread owns one key's
+// 32 logits and, at the end, one d of the 32 outputs.
+//
+// The weights P need more than one 8-bit (or bf16) operand to keep their
+// precision.  e4m3 caches: w is rounded to fp16 (11 bits) and cut into four e5m2
+// terms of 3 + 3 + 3 + 2 bits, each the upper byte of what is left (e5m2 is fp16's
+// upper half, so the cut is a mask and the rest an exact subtraction), which sum
+// to the fp16 value down to 2^-16, that is 2^-31 of the row's largest.  bf16 caches:
+// two bf16 terms.  The terms are columns of one product, so V is read once; their
+// accumulators are added when the segment ends.
+//
+// Keys that only some of the tile's tokens see (at most 15, the new ones) stay out
+// of the tiles, where a weight of 0 would not keep a value that is not finite out
+// of the other rows' sums: they are added row by row when an item ends.
+//
+// Warps 0-3: softmax (a thread a key); warp 4: copies; warp 5: products.  They
+// meet in mbarriers only, so that the copies run on into the next segment.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp2_decode.cuh"
+
+namespace fp2 {
+
+namespace {
+
+constexpr int kTileKeys = 128, kTileRows = 32, kTileWarps = 6, kTileThreads = 32 * kTileWarps;
+
+template <bool FP8>
+struct Tile {
+    static constexpr int DH = 128;
+    static constexpr int RB = DH * (FP8 ? 1 : 2);
+    static constexpr int HALVES = RB / 128;               // 128-byte columns of a row
+    static constexpr int HALF = kTileKeys * 128;          // bytes of one
+    static constexpr int STAGE = 2 * HALVES * HALF;       // K, then V
+    static constexpr int STAGES = FP8 ? 2 : 3;
+    static constexpr int TERMS = FP8 ? 4 : 2;             // operand terms of a weight
+    static constexpr int PV_N = TERMS * kTileRows;        // columns of the second product: 128 bytes a key
+    static constexpr int KSTEP = FP8 ? 32 : 16;           // k of one product
+    static constexpr int OFF_P = STAGES * STAGE;
+    static constexpr int OFF_Q = OFF_P + HALF;
+    static constexpr int SMEM = OFF_Q + HALVES * kTileRows * 128;
+    static constexpr int O_COL = 64;                      // TMEM: S twice, then O
+    static constexpr uint32_t TMEM = FP8 ? 256 : 128;
+    static constexpr int PER_SM = FP8 ? 2 : 1;
+    static constexpr int CTAS = 148 * PER_SM;
+    static_assert(O_COL + PV_N <= (int)TMEM, "TMEM");
+};
+
+enum { T_FULL = 0, T_EMPTY = 3, T_S_FULL = 6, T_S_FREE = 8, T_P_READY = 10, T_O_DONE, T_Q_READY, T_DRAIN, T_COUNT };
+enum { kDetTileCopy = kDetWaitBase + 8, kDetTileMma, kDetTileSoftmax };
+
+// Instruction descriptor with fp32 accumulation: operand formats a, b (kind::f16:
+// 1 = bf16; kind::f8f6f4: 0 = e4m3, 1 = e5m2), MN-major operands, 128 x n.
+__host__ __device__ constexpr uint32_t tile_idesc(uint32_t a, uint32_t b, bool mn_major, int n) {
+    return (1u << 4) | (a << 7) | (b << 10) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Barrier of the four softmax warps, and whether `x` holds in any thread.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// Lane i gets the reduction of v[i] over the warp's lanes.
+template <typename Op>
+__device__ __forceinline__ float reduce32(float (&v)[32], Op op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int half = 16; half > 0; half >>= 1) {
+        const bool up = lane & half;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+            v[i] = op(keep, __shfl_xor_sync(~0u, send, half));
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ float2 e4m3_pair(uint16_t x) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    return __half22float2(*reinterpret_cast<__half2*>(&y));
+}
+// q . k of one row each, in fp32.
+template <bool FP8>
+__device__ __forceinline__ float dot_row(const uint8_t* q, const uint8_t* k) {
+    float z = 0.f;
+    for (int i = 0; i < Tile<FP8>::RB; i += 16) {
+        const uint4 a = *reinterpret_cast<const uint4*>(q + i), b = *reinterpret_cast<const uint4*>(k + i);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (FP8) {
+                const float2 a0 = e4m3_pair((uint16_t)x[e]), a1 = e4m3_pair((uint16_t)(x[e] >> 16));
+                const float2 b0 = e4m3_pair((uint16_t)y[e]), b1 = e4m3_pair((uint16_t)(y[e] >> 16));
+                z += a0.x * b0.x + a0.y * b0.y + a1.x * b1.x + a1.y * b1.y;
+            } else {
+                z += __uint_as_float(x[e] << 16) * __uint_as_float(y[e] << 16) +
+                     __uint_as_float(x[e] & 0xFFFF0000u) * __uint_as_float(y[e] & 0xFFFF0000u);
+            }
+        }
+    }
+    return z;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
+    decode_tiles_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ DecodeMaps maps) {
+    using C = Tile<FP8>;
+    constexpr int R = kTileRows, DH = C::DH, RB = C::RB, STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[T_COUNT];
+    __shared__ uint32_t tmem_at;
+    __shared__ int aborted;
+    __shared__ float sm_red[4][R], sm_m[R], sm_l[R], sm_f[R], sm_w[16][R], sm_sc[R], sm_nm[R];
+    const KParams& p = D.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // adjacent CTAs take the heads of a group over the same keys, so that a token's
+    // rows of both are read at about the same time
+    const int c = blockIdx.x / D.hc, hs = blockIdx.x % D.hc;
+    const uint32_t base = smem_u32(smem);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T_COUNT; ++i)
+            mbar_init(&bars[i], i == T_S_FREE || i == T_S_FREE + 1 || i == T_P_READY || i == T_Q_READY ? 128 : 1);
+        fence_mbar_init();
+        aborted = 0;
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
+    wait_previous();
+    Share x;
+    if (!find_share<R, kTileKeys, kTileWarps>(D, c, gridDim.x / D.hc, 1, hs == 0, x)) return;
+    if (warp == 5) {
+        tmem_alloc(&tmem_at, C::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    Segment g;
+    int t = 0;  // tiles before the present one, over all segments: stages and phases follow it
+    auto stage_of = [&](int i) { return base + (i % STAGES) * C::STAGE; };
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ copies ---
+        bool ok = true;
+        while (ok && next_segment<R, kTileKeys>(D, x, g)) {
+            const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
+            // lane 8 i + j: cache row of box j of tile 4 k + i, a round of 4 tiles ahead
+            auto rows_of = [&](int n) {
+                const int tile = n + (lane >> 3), key = (g.x0 + tile) * kTileKeys + (lane & 7) * kDecBox;
+                return tile < n_tiles && key < g.seen_all ? (int)key_row(p, x.s, x.b, key) : -1;
+            };
+            int now = rows_of(0), next = rows_of(4);
+            for (int n = 0; n < n_tiles; ++n, ++t) {
+                if (n > 0 && (n & 3) == 0) {
+                    now = next;
+                    next = rows_of(n + 4);
+                }
+                const int st = t % STAGES;
+                if (t >= STAGES &&
+                    !__all_sync(~0u, mbar_wait(&bars[T_EMPTY + st], (t / STAGES - 1) & 1, &aborted, kDecWaitNs))) {
+                    if (lane == 0) set_error(p.err, kErrTimeout, kDetTileCopy);
+                    ok = false;
+                    break;
+                }
+                const bool mine = (lane >> 3) == (n & 3) && now >= 0;
+                const int boxes = __popc(__ballot_sync(~0u, mine));
+                if (lane == 0) mbar_arrive_expect_tx(&bars[T_FULL + st], boxes * kDecBox * RB * 2);
+                __syncwarp();
+                if (mine) {
+                    const uint32_t dst = stage_of(t) + (lane & 7) * kDecBox * 128;
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h) {
+                        tma_load_3d(dst + h * C::HALF, &maps.k, &bars[T_FULL + st], h * (FP8 ? 128 : 64), hk, now);
+                        tma_load_3d(dst + (C::HALVES + h) * C::HALF, &maps.v, &bars[T_FULL + st], h * (FP8 ? 128 : 64), hk, now);
+                    }
+                }
+            }
+            x.u = g.item_at + g.x1;
+        }
+        // never leave with copies in flight
+        int ignore = 0;
+        for (int i = max(0, t - STAGES); i < t; ++i)
+            mbar_wait(&bars[T_FULL + i % STAGES], (i / STAGES) & 1, &ignore, kDecWaitNs);
+    } else if (warp == 5) {
+        // ---------------------------------------------------------- products ---
+        if (lane == 0) {
+            constexpr uint32_t fmt = FP8 ? 0u : 1u;
+            constexpr uint32_t idesc_qk = tile_idesc(fmt, fmt, false, R);
+            constexpr uint32_t idesc_pv = tile_idesc(fmt, 1u, true, C::PV_N);  // e4m3 x e5m2, bf16 x bf16
+            bool ok = true;
+            for (int seg = 0; ok && next_segment<R, kTileKeys>(D, x, g); ++seg) {
+                const int n_tiles = g.x1 - g.x0;
+                ok = mbar_wait(&bars[T_Q_READY], seg & 1, &aborted, kDecWaitNs);
+                for (int n = 0; ok && n <= n_tiles; ++n) {
+                    if (n < n_tiles) {
+                        const int i = t + n, st = i % STAGES, buf = i & 1;
+                        ok = mbar_wait(&bars[T_FULL + st], (i / STAGES) & 1, &aborted, kDecWaitNs) &&
+                             (i < 2 || mbar_wait(&bars[T_S_FREE + buf], (i / 2 - 1) & 1, &aborted, kDecWaitNs));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < DH / C::KSTEP; ++ks) {  // 32 bytes of d each
+                            const uint64_t ad = sw128_desc(stage_of(i) + (ks >> 2) * C::HALF + (ks & 3) * 32, 16, 1024);
+                            const uint64_t bd = sw128_desc(base + C::OFF_Q + (ks >> 2) * R * 128 + (ks & 3) * 32, 16, 1024);
+                            if constexpr (FP8) mma_f8_ss(tmem + buf * R, ad, bd, idesc_qk, ks > 0);
+                            else mma_bf16_ss(tmem + buf * R, ad, bd, idesc_qk, ks > 0);
+                        }
+                        mma_commit(&bars[T_S_FULL + buf]);
+                    }
+                    if (n >= 1) {
+                        const int i = t + n - 1;
+                        ok = mbar_wait(&bars[T_P_READY], i & 1, &aborted, kDecWaitNs);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < kTileKeys / C::KSTEP; ++ks) {  // KSTEP keys each
+                            const uint64_t ad = sw128_desc(stage_of(i) + C::HALVES * C::HALF + ks * C::KSTEP * 128, C::HALF, 1024);
+                            const uint64_t bd = sw128_desc(base + C::OFF_P + ks * C::KSTEP * 128, C::HALF, 1024);
+                            const uint32_t acc = n > 1 || ks > 0;
+                            if constexpr (FP8) mma_f8_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
+                            else mma_bf16_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
+                        }
+                        mma_commit(&bars[T_O_DONE]);
+                        mma_commit(&bars[T_EMPTY + i % STAGES]);
+                    }
+                }
+                t += n_tiles;
+                x.u = g.item_at + g.x1;
+            }
+            if (!ok) set_error(p.err, kErrTimeout, kDetTileMma);
+            // every product is done before TMEM is given back
+            mma_commit(&bars[T_DRAIN]);
+            int ignore = 0;
+            mbar_wait(&bars[T_DRAIN], 0, &ignore, kDecWaitNs);
+        }
+    } else {
+        // ----------------------------------------------------------- softmax ---
+        const int tid = threadIdx.x;  // key of the tile, TMEM lane; d of the output
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        uint8_t* const p_row = smem + C::OFF_P + tid * 128;
+        bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
+        while (!dead && next_segment<R, kTileKeys>(D, x, g)) {
+            const SeqInfo& s = x.s;
+            const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
+            auto token = [&](int r) { return (g.tile * R + r) / p.G; };
+            auto head = [&](int r) { return hk * p.G + (g.tile * R + r) % p.G; };
+            auto q_row = [&](int r) {
+                return static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * RB;
+            };
+            for (int i = tid; i < R * RB / 16; i += 128) {  // Q tile, swizzled, rows past the last 0
+                const int r = i / (RB / 16), ch = i % (RB / 16);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (r < g.rows) v = *reinterpret_cast<const uint4*>(q_row(r) + ch * 16);
+                *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * R * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars[T_Q_READY]);
+            float l[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) l[r] = 0.f;
+            if (tid < R) {
+                sm_nm[tid] = FLT_MAX;  // minus the row's reference
+                // a logit's factor: rows differ by their head's scale
+                if (FP8) sm_sc[tid] = D.qk_scale * p.k_scale[hk] * p.q_scale[head(min(tid, g.rows - 1))];
+            }
+            softmax_sync();
+            auto factors = [&](int n) {  // of tile n's key block
+                float2 f = make_float2(1.f, 1.f);
+                if (FP8 && p.kb_fac && n < n_tiles) {
+                    const size_t at = ((size_t)x.b * p.nkb_max + g.x0 + n) * p.Hkv + hk;
+                    f = make_float2(p.kb_fac[at], p.vb_fac[at]);
+                    if (!(f.x > 0.f && f.x <= 1.f && f.y > 0.f && f.y <= 1.f)) {
+                        set_error(p.err, kErrInvalid, kDetFactor);
+                        f = make_float2(1.f, 1.f);
+                    }
+                }
+                return f;
+            };
+            float2 fac_next = factors(0);
+            for (int n = 0; n < n_tiles; ++n, ++t) {
+                const int buf = t & 1, j0 = (g.x0 + n) * kTileKeys;
+                const float2 fac = fac_next;
+                fac_next = factors(n + 1);
+                ok = mbar_wait(&bars[T_S_FULL + buf], (t >> 1) & 1, &aborted, kDecWaitNs) && ok;
+                __syncwarp();
+                tc_fence_after();
+                const bool seen = j0 + tid < g.seen_all;
+                auto factor = [&](int r) { return FP8 ? sm_sc[r] * fac.x : D.qk_scale; };
+                float w[R], top = -FLT_MAX;
+                tmem_ld32f(tmem + lanes + buf * R, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    w[r] = fmaf(w[r], factor(r), sm_nm[r]);
+                    top = fmaxf(top, w[r]);
+                }
+                if (softmax_any((seen && top > kRoof) || !ok)) {
+                    if (softmax_any(!ok)) {
+                        dead = true;
+                        break;
+                    }
+                    // the references move: each row's largest z over the tile's keys
+                    tmem_ld32f(tmem + lanes + buf * R, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int r = 0; r < R; ++r) w[r] = seen ? w[r] * factor(r) : -INFINITY;
+                    sm_red[warp][lane] = reduce32(w, [](float a, float b) { return fmaxf(a, b); });
+                    softmax_sync();
+                    if (tid < R) {
+                        const float most = fmaxf(fmaxf(sm_red[0][tid], sm_red[1][tid]), fmaxf(sm_red[2][tid], sm_red[3][tid]));
+                        const float old = sm_nm[tid];
+                        const bool moves = most + old > kRoof;
+                        sm_f[tid] = moves ? ex2(kLift - most - old) : 1.f;
+                        if (moves) sm_nm[tid] = kLift - most;
+                    }
+                    softmax_sync();
+#pragma unroll
+                    for (int r = 0; r < R; ++r) l[r] *= sm_f[r];
+                    if (n > 0) {
+                        ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < C::TERMS; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + lanes + C::O_COL + k * R, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < R; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sm_f[r]);
+                            tmem_st32(tmem + lanes + C::O_COL + k * R, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    tmem_ld32f(tmem + lanes + buf * R, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int r = 0; r < R; ++r) w[r] = fmaf(w[r], factor(r), sm_nm[r]);
+                }
+                tc_fence_before();
+                mbar_arrive(&bars[T_S_FREE + buf]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    w[r] = seen ? ex2(w[r]) : 0.f;
+                    l[r] += w[r];
+                }
+                if (n > 0) {  // the product before has read P
+                    ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
+                    __syncwarp();
+                }
+                if constexpr (FP8) {
+                    uint32_t left[R / 2];  // fp16 pairs: what the terms so far leave
+#pragma unroll
+                    for (int i = 0; i < R / 2; ++i) {
+                        const float f = p.kb_fac ? fac.y : 1.f;
+                        asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(left[i]) : "f"(w[2 * i] * f), "f"(w[2 * i + 1] * f));
+                    }
+#pragma unroll
+                    for (int k = 0; k < C::TERMS; ++k) {
+                        uint32_t cut[R / 2];
+#pragma unroll
+                        for (int i = 0; i < R / 2; ++i) {
+                            cut[i] = left[i] & 0xFF00FF00u;
+                            if (k + 1 < C::TERMS) asm("sub.f16x2 %0, %0, %1;" : "+r"(left[i]) : "r"(cut[i]));
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = __byte_perm(cut[8 * h + 2 * e], cut[8 * h + 2 * e + 1], 0x7531);
+                            *reinterpret_cast<uint4*>(p_row + (((2 * k + h) ^ (tid & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = w[8 * ch + 2 * e], b = w[8 * ch + 2 * e + 1];
+                            hi[e] = pack_bf16x2(a, b);
+                            lo[e] = pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xFFFF0000u));
+                        }
+                        *reinterpret_cast<uint4*>(p_row + ((ch ^ (tid & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(p_row + (((4 + ch) ^ (tid & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                if (j0 + kTileKeys > g.seen_all && !seen) {
+                    // rows of V that are none of these rows' values: finite
+                    uint8_t* v = smem + (t % STAGES) * C::STAGE + C::HALVES * C::HALF + tid * 128;
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(v + h * C::HALF + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(&bars[T_P_READY]);
+            }
+            if (dead) break;
+
+            // ------------------------------------------- the segment's result ---
+            ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
+            __syncwarp();
+            if (softmax_any(!ok)) {
+                dead = true;
+                break;
+            }
+            tc_fence_after();
+            float o[R];
+#pragma unroll
+            for (int k = 0; k < C::TERMS; ++k) {
+                float y[R];
+                tmem_ld32f(tmem + lanes + C::O_COL + k * R, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < R; ++r) o[r] = k ? o[r] + y[r] : y[r];
+            }
+            tc_fence_before();
+            sm_red[warp][lane] = reduce32(l, [](float a, float b) { return a + b; });
+            // the keys that not every row sees, where the item ends
+            const int tail = g.x1 == g.per_item ? g.seen_any - g.seen_all : 0;
+            auto tail_factor = [&](int j, bool of_v) {
+                if (!FP8 || !p.kb_fac) return 1.f;
+                const size_t at = ((size_t)x.b * p.nkb_max + j / p.B) * p.Hkv + hk;
+                return of_v ? p.vb_fac[at] : p.kb_fac[at];
+            };
+            for (int i = tid; i < tail * R; i += 128) {
+                const int r = i % R, j = g.seen_all + i / R;
+                float z = -INFINITY;
+                if (r < g.rows && j <= s.P + token(r)) {
+                    const long long row = key_row(p, s, x.b, j);
+                    const float f = D.qk_scale * (FP8 ? p.k_scale[hk] * p.q_scale[head(r)] : 1.f) * tail_factor(j, false);
+                    if (row >= 0) z = f * dot_row<FP8>(q_row(r), static_cast<const uint8_t*>(D.k) + (row * p.Hkv + hk) * RB);
+                }
+                sm_w[i / R][r] = z;
+            }
+            softmax_sync();
+            if (tid < R) {
+                const float m = -sm_nm[tid];
+                float most = m, sum = sm_red[0][tid] + sm_red[1][tid] + sm_red[2][tid] + sm_red[3][tid];
+                for (int k = 0; k < tail; ++k) most = fmaxf(most, sm_w[k][tid]);
+                const float f = ex2(m - most);
+                sum *= f;
+                for (int k = 0; k < tail; ++k) {
+                    const float w = ex2(sm_w[k][tid] - most);
+                    sum += w;
+                    sm_w[k][tid] = w * tail_factor(g.seen_all + k, true);
+                }
+                sm_m[tid] = most;
+                sm_l[tid] = sum;
+                sm_f[tid] = f;
+            }
+            softmax_sync();
+            if (tail > 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) o[r] *= sm_f[r];
+                for (int k = 0; k < tail; ++k) {
+                    const int j = g.seen_all + k;
+                    const long long row = key_row(p, s, x.b, j);
+                    if (row < 0) continue;
+                    const long long at = (row * p.Hkv + hk) * DH + tid;
+                    float v;
+                    if constexpr (FP8) v = e4m3_pair(static_cast<const uint8_t*>(D.v)[at]).x;
+                    else v = __bfloat162float(static_cast<const __nv_bfloat16*>(D.v)[at]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (r < g.rows && j <= s.P + token(r)) o[r] = fmaf(sm_w[k][r], v, o[r]);
+                }
+            }
+            const int slot = 2 * c + (g.x0 == 0 ? 1 : 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r >= g.rows) break;
+                if (g.whole()) {
+                    const float y = o[r] * ((FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]);
+                    const long long at = ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * DH + tid;
+                    if (p.out_fp8) {
+                        const float unit = p.out_scale ? p.out_scale[head(r)] : p.v_scale[hk];
+                        static_cast<uint8_t*>(D.out)[at] = (uint8_t)pack_e4m3x4(y / unit, 0.f, 0.f, 0.f);
+                    } else {
+                        static_cast<__nv_bfloat16*>(D.out)[at] = __float2bfloat16(y);
+                    }
+                } else {
+                    D.part[(((size_t)slot * D.hc + hs) * R + r) * DH + tid] = o[r];
+                }
+            }
+            if (tid < g.rows) {
+                if (g.whole()) {
+                    if (D.lse) D.lse[(long long)(s.q0 + token(tid)) * p.Hq + head(tid)] = lse_of(sm_m[tid], sm_l[tid]);
+                } else {
+                    const size_t at = ((size_t)slot * D.hc + hs) * R + tid;
+                    *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[tid], sm_l[tid]);
+                }
+            }
+            if (tid == 0 && hs == 0) put_record(D, x, g, c);
+            softmax_sync();  // sm_* are free for the next segment
+            x.u = g.item_at + g.x1;
+        }
+        if (dead && lane == 0) set_error(p.err, kErrTimeout, kDetTileSoftmax);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
+template <bool FP8>
+cudaError_t launch(const DecodeParams& D, cudaStream_t s) {
+    using C = Tile<FP8>;
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = allow_smem(decode_tiles_kernel<FP8>, C::SMEM, ready);
+    if (e != cudaSuccess) return e;
+    DecodeMaps maps;
+    const bool wide = D.hc * C::RB >= 256 || D.p.Hkv == 1;
+    if (!make_row_maps(D.p, D.k, D.v, kDecBox, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
+    return launch_early(decode_tiles_kernel<FP8>, dim3(C::CTAS), kTileThreads, C::SMEM, s, D, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tiles(const DecodeParams& D, cudaStream_t s) {
+    return D.p.fp8 ? launch<true>(D, s) : launch<false>(D, s);
+}
+int decode_tile_shares(const DecodeParams& D) { return (D.p.fp8 ? Tile<true>::CTAS : Tile<false>::CTAS) / D.hc; }
+
+}  // namespace fp2
