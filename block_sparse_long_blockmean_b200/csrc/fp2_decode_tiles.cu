@@ -6,7 +6,7 @@
 //   S^T (128 keys x 32 rows)  = K (128 x d) Q^T           both K-major
 //   O^T (128 d x 32 rows)    += V^T (d x 128 keys) P^T    both MN-major, as stored
 // so that neither K nor V is transposed or converted; a thread owns one key's
-// 32 logits and, at the end, one d of the 32 outputs.
+// logits of 16 rows and, at the end, one d of their outputs.
 //
 // The weights P need more than one 8-bit (or bf16) operand to keep their
 // precision.  e4m3 caches: w is rounded to fp16 (11 bits) and cut into four e5m2
@@ -20,8 +20,9 @@
 // of the tiles, where a weight of 0 would not keep a value that is not finite out
 // of the other rows' sums: they are added row by row when an item ends.
 //
-// Warps 0-3: softmax (a thread a key); warp 4: copies; warp 5: products.  They
-// meet in mbarriers only, so that the copies run on into the next segment.
+// Warps 0-3 and 4-7: softmax of rows 0-15 and 16-31 (a thread a key); warp 8:
+// copies; warp 9: products.  They meet in mbarriers only, so that the copies run on
+// into the next segment.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,7 +32,8 @@ namespace fp2 {
 
 namespace {
 
-constexpr int kTileKeys = 128, kTileRows = 32, kTileWarps = 6, kTileThreads = 32 * kTileWarps;
+constexpr int kTileKeys = 128, kTileRows = 32, kTileWarps = 10, kTileThreads = 32 * kTileWarps;
+constexpr int kHalfRows = kTileRows / 2;  // of a softmax warpgroup
 
 template <bool FP8>
 struct Tile {
@@ -40,7 +42,7 @@ struct Tile {
     static constexpr int HALVES = RB / 128;               // 128-byte columns of a row
     static constexpr int HALF = kTileKeys * 128;          // bytes of one
     static constexpr int STAGE = 2 * HALVES * HALF;       // K, then V
-    static constexpr int STAGES = FP8 ? 2 : 3;
+    static constexpr int STAGES = FP8 ? 6 : 3;
     static constexpr int TERMS = FP8 ? 4 : 2;             // operand terms of a weight
     static constexpr int PV_N = TERMS * kTileRows;        // columns of the second product: 128 bytes a key
     static constexpr int KSTEP = FP8 ? 32 : 16;           // k of one product
@@ -49,12 +51,11 @@ struct Tile {
     static constexpr int SMEM = OFF_Q + HALVES * kTileRows * 128;
     static constexpr int O_COL = 64;                      // TMEM: S twice, then O
     static constexpr uint32_t TMEM = FP8 ? 256 : 128;
-    static constexpr int PER_SM = FP8 ? 2 : 1;
-    static constexpr int CTAS = 148 * PER_SM;
-    static_assert(O_COL + PV_N <= (int)TMEM, "TMEM");
+    static constexpr int CTAS = 148;                      // one on each SM
+    static_assert(O_COL + PV_N <= (int)TMEM && SMEM <= 224 * 1024, "on-chip memory");
 };
 
-enum { T_FULL = 0, T_EMPTY = 3, T_S_FULL = 6, T_S_FREE = 8, T_P_READY = 10, T_O_DONE, T_Q_READY, T_DRAIN, T_COUNT };
+enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE, T_Q_READY, T_DRAIN, T_COUNT };
 enum { kDetTileCopy = kDetWaitBase + 8, kDetTileMma, kDetTileSoftmax };
 
 // Instruction descriptor with fp32 accumulation: operand formats a, b (kind::f16:
@@ -63,32 +64,48 @@ __host__ __device__ constexpr uint32_t tile_idesc(uint32_t a, uint32_t b, bool m
     return (1u << 4) | (a << 7) | (b << 10) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Barrier of the four softmax warps, and whether `x` holds in any thread.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
+// Barrier of a softmax warpgroup, and whether `x` holds in any of its threads.
+__device__ __forceinline__ void softmax_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
+__device__ __forceinline__ bool softmax_any(int wg, bool x) {
     uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x)
+        : "r"((uint32_t)x), "r"(1 + wg)
         : "memory");
     return r != 0;
 }
 
-// Lane i gets the reduction of v[i] over the warp's lanes.
+// Lanes 2 i and 2 i + 1 get the reduction of v[i] over the warp's lanes.
 template <typename Op>
-__device__ __forceinline__ float reduce32(float (&v)[32], Op op) {
+__device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int half = 16; half > 0; half >>= 1) {
-        const bool up = lane & half;
+    for (int half = 8; half > 0; half >>= 1) {
+        const bool up = lane & (2 * half);
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(~0u, send, half));
+            v[i] = op(keep, __shfl_xor_sync(~0u, send, 2 * half));
         }
     }
-    return v[0];
+    return op(v[0], __shfl_xor_sync(~0u, v[0], 1));
+}
+
+// 32 lanes x 16 consecutive 32-bit TMEM columns.
+__device__ __forceinline__ void tmem_ld16f(uint32_t at, float (&f)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]),
+          "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_st16f(uint32_t at, const float (&f)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "f"(f[8]), "f"(f[9]), "f"(f[10]),
+        "f"(f[11]), "f"(f[12]), "f"(f[13]), "f"(f[14]), "f"(f[15])
+        : "memory");
 }
 
 __device__ __forceinline__ float2 e4m3_pair(uint16_t x) {
@@ -119,7 +136,7 @@ __device__ __forceinline__ float dot_row(const uint8_t* q, const uint8_t* k) {
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
+__global__ void __launch_bounds__(kTileThreads, 1)
     decode_tiles_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ DecodeMaps maps) {
     using C = Tile<FP8>;
     constexpr int R = kTileRows, DH = C::DH, RB = C::RB, STAGES = C::STAGES;
@@ -127,7 +144,7 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
     __shared__ __align__(8) uint64_t bars[T_COUNT];
     __shared__ uint32_t tmem_at;
     __shared__ int aborted;
-    __shared__ float sm_red[4][R], sm_m[R], sm_l[R], sm_f[R], sm_w[16][R], sm_sc[R], sm_nm[R];
+    __shared__ float sm_red[8][kHalfRows], sm_m[R], sm_l[R], sm_f[R], sm_w[16][R], sm_sc[R], sm_nm[R];
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // adjacent CTAs take the heads of a group over the same keys, so that a token's
@@ -136,7 +153,7 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
-            mbar_init(&bars[i], i == T_S_FREE || i == T_S_FREE + 1 || i == T_P_READY || i == T_Q_READY ? 128 : 1);
+            mbar_init(&bars[i], i == T_S_FREE || i == T_S_FREE + 1 || i == T_P_READY || i == T_Q_READY ? 256 : 1);
         fence_mbar_init();
         aborted = 0;
         prefetch_tmap(&maps.k);
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
     wait_previous();
     Share x;
     if (!find_share<R, kTileKeys, kTileWarps>(D, c, gridDim.x / D.hc, 1, hs == 0, x)) return;
-    if (warp == 5) {
+    if (warp == 9) {
         tmem_alloc(&tmem_at, C::TMEM);
         tmem_relinquish();
     }
@@ -157,7 +174,7 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
     int t = 0;  // tiles before the present one, over all segments: stages and phases follow it
     auto stage_of = [&](int i) { return base + (i % STAGES) * C::STAGE; };
 
-    if (warp == 4) {
+    if (warp == 8) {
         // ------------------------------------------------------------ copies ---
         bool ok = true;
         while (ok && next_segment<R, kTileKeys>(D, x, g)) {
@@ -199,7 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
         int ignore = 0;
         for (int i = max(0, t - STAGES); i < t; ++i)
             mbar_wait(&bars[T_FULL + i % STAGES], (i / STAGES) & 1, &ignore, kDecWaitNs);
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         // ---------------------------------------------------------- products ---
         if (lane == 0) {
             constexpr uint32_t fmt = FP8 ? 0u : 1u;
@@ -253,8 +270,11 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
         }
     } else {
         // ----------------------------------------------------------- softmax ---
-        const int tid = threadIdx.x;  // key of the tile, TMEM lane; d of the output
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        constexpr int H = kHalfRows;
+        const int wg = warp >> 2, w4 = warp & 3, first = wg * H;  // rows first + 0 .. H - 1
+        const int tid = threadIdx.x & 127;  // key of the tile, TMEM lane; d of the output
+        const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+        float(*const red)[H] = sm_red + 4 * wg;
         uint8_t* const p_row = smem + C::OFF_P + tid * 128;
         bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
         while (!dead && next_segment<R, kTileKeys>(D, x, g)) {
@@ -265,139 +285,135 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
             auto q_row = [&](int r) {
                 return static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * RB;
             };
-            for (int i = tid; i < R * RB / 16; i += 128) {  // Q tile, swizzled, rows past the last 0
-                const int r = i / (RB / 16), ch = i % (RB / 16);
+            for (int i = tid; i < H * RB / 16; i += 128) {  // Q tile, swizzled, rows past the last 0
+                const int r = first + i / (RB / 16), ch = i % (RB / 16);
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (r < g.rows) v = *reinterpret_cast<const uint4*>(q_row(r) + ch * 16);
                 *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * R * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars[T_Q_READY]);
-            float l[R];
+            float l[H];
 #pragma unroll
-            for (int r = 0; r < R; ++r) l[r] = 0.f;
-            if (tid < R) {
-                sm_nm[tid] = FLT_MAX;  // minus the row's reference
+            for (int i = 0; i < H; ++i) l[i] = 0.f;
+            if (tid < H) {
+                sm_nm[first + tid] = FLT_MAX;  // minus the row's reference
                 // a logit's factor: rows differ by their head's scale
-                if (FP8) sm_sc[tid] = D.qk_scale * p.k_scale[hk] * p.q_scale[head(min(tid, g.rows - 1))];
+                if (FP8) sm_sc[first + tid] = D.qk_scale * p.k_scale[hk] * p.q_scale[head(min(first + tid, g.rows - 1))];
             }
-            softmax_sync();
-            auto factors = [&](int n) {  // of tile n's key block
-                float2 f = make_float2(1.f, 1.f);
-                if (FP8 && p.kb_fac && n < n_tiles) {
-                    const size_t at = ((size_t)x.b * p.nkb_max + g.x0 + n) * p.Hkv + hk;
-                    f = make_float2(p.kb_fac[at], p.vb_fac[at]);
-                    if (!(f.x > 0.f && f.x <= 1.f && f.y > 0.f && f.y <= 1.f)) {
-                        set_error(p.err, kErrInvalid, kDetFactor);
-                        f = make_float2(1.f, 1.f);
-                    }
-                }
-                return f;
+            softmax_sync(wg);
+            auto factors = [&](int n) {  // of tile n's key block; used a tile later
+                if (!FP8 || !p.kb_fac || n >= n_tiles) return make_float2(1.f, 1.f);
+                const size_t at = ((size_t)x.b * p.nkb_max + g.x0 + n) * p.Hkv + hk;
+                return make_float2(p.kb_fac[at], p.vb_fac[at]);
             };
             float2 fac_next = factors(0);
             for (int n = 0; n < n_tiles; ++n, ++t) {
                 const int buf = t & 1, j0 = (g.x0 + n) * kTileKeys;
-                const float2 fac = fac_next;
+                float2 fac = fac_next;
                 fac_next = factors(n + 1);
+                if (FP8 && !(fac.x > 0.f && fac.x <= 1.f && fac.y > 0.f && fac.y <= 1.f)) {
+                    set_error(p.err, kErrInvalid, kDetFactor);
+                    fac = make_float2(1.f, 1.f);
+                }
                 ok = mbar_wait(&bars[T_S_FULL + buf], (t >> 1) & 1, &aborted, kDecWaitNs) && ok;
                 __syncwarp();
                 tc_fence_after();
                 const bool seen = j0 + tid < g.seen_all;
-                auto factor = [&](int r) { return FP8 ? sm_sc[r] * fac.x : D.qk_scale; };
-                float w[R], top = -FLT_MAX;
-                tmem_ld32f(tmem + lanes + buf * R, w);
+                auto factor = [&](int i) { return FP8 ? sm_sc[first + i] * fac.x : D.qk_scale; };
+                const uint32_t s_at = tmem + lanes + buf * R + first;
+                float w[H], top = -FLT_MAX;
+                tmem_ld16f(s_at, w);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    w[r] = fmaf(w[r], factor(r), sm_nm[r]);
-                    top = fmaxf(top, w[r]);
+                for (int i = 0; i < H; ++i) {
+                    w[i] = fmaf(w[i], factor(i), sm_nm[first + i]);
+                    top = fmaxf(top, w[i]);
                 }
-                if (softmax_any((seen && top > kRoof) || !ok)) {
-                    if (softmax_any(!ok)) {
+                if (softmax_any(wg, (seen && top > kRoof) || !ok)) {
+                    if (softmax_any(wg, !ok)) {
                         dead = true;
                         break;
                     }
                     // the references move: each row's largest z over the tile's keys
-                    tmem_ld32f(tmem + lanes + buf * R, w);
+                    tmem_ld16f(s_at, w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < R; ++r) w[r] = seen ? w[r] * factor(r) : -INFINITY;
-                    sm_red[warp][lane] = reduce32(w, [](float a, float b) { return fmaxf(a, b); });
-                    softmax_sync();
-                    if (tid < R) {
-                        const float most = fmaxf(fmaxf(sm_red[0][tid], sm_red[1][tid]), fmaxf(sm_red[2][tid], sm_red[3][tid]));
-                        const float old = sm_nm[tid];
+                    for (int i = 0; i < H; ++i) w[i] = seen ? w[i] * factor(i) : -INFINITY;
+                    const float top_of = reduce16(w, [](float a, float b) { return fmaxf(a, b); });
+                    red[w4][lane >> 1] = top_of;
+                    softmax_sync(wg);
+                    if (tid < H) {
+                        const float most = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
+                        const float old = sm_nm[first + tid];
                         const bool moves = most + old > kRoof;
-                        sm_f[tid] = moves ? ex2(kLift - most - old) : 1.f;
-                        if (moves) sm_nm[tid] = kLift - most;
+                        sm_f[first + tid] = moves ? ex2(kLift - most - old) : 1.f;
+                        if (moves) sm_nm[first + tid] = kLift - most;
                     }
-                    softmax_sync();
+                    softmax_sync(wg);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) l[r] *= sm_f[r];
+                    for (int i = 0; i < H; ++i) l[i] *= sm_f[first + i];
                     if (n > 0) {
                         ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
                         for (int k = 0; k < C::TERMS; ++k) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + lanes + C::O_COL + k * R, o);
+                            const uint32_t o_at = tmem + lanes + C::O_COL + k * R + first;
+                            tmem_ld16f(o_at, w);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int r = 0; r < R; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sm_f[r]);
-                            tmem_st32(tmem + lanes + C::O_COL + k * R, o);
+                            for (int i = 0; i < H; ++i) w[i] *= sm_f[first + i];
+                            tmem_st16f(o_at, w);
                         }
                         tmem_wait_st();
                     }
-                    tmem_ld32f(tmem + lanes + buf * R, w);
+                    tmem_ld16f(s_at, w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < R; ++r) w[r] = fmaf(w[r], factor(r), sm_nm[r]);
+                    for (int i = 0; i < H; ++i) w[i] = fmaf(w[i], factor(i), sm_nm[first + i]);
                 }
                 tc_fence_before();
                 mbar_arrive(&bars[T_S_FREE + buf]);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    w[r] = seen ? ex2(w[r]) : 0.f;
-                    l[r] += w[r];
+                for (int i = 0; i < H; ++i) {
+                    w[i] = seen ? ex2(w[i]) : 0.f;
+                    l[i] += w[i];
                 }
                 if (n > 0) {  // the product before has read P
                     ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
                     __syncwarp();
                 }
                 if constexpr (FP8) {
-                    uint32_t left[R / 2];  // fp16 pairs: what the terms so far leave
+                    uint32_t left[H / 2];  // fp16 pairs: what the terms so far leave
 #pragma unroll
-                    for (int i = 0; i < R / 2; ++i) {
+                    for (int i = 0; i < H / 2; ++i) {
                         const float f = p.kb_fac ? fac.y : 1.f;
                         asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(left[i]) : "f"(w[2 * i] * f), "f"(w[2 * i + 1] * f));
                     }
 #pragma unroll
                     for (int k = 0; k < C::TERMS; ++k) {
-                        uint32_t cut[R / 2];
+                        uint32_t cut[H / 2], v[4];
 #pragma unroll
-                        for (int i = 0; i < R / 2; ++i) {
+                        for (int i = 0; i < H / 2; ++i) {
                             cut[i] = left[i] & 0xFF00FF00u;
                             if (k + 1 < C::TERMS) asm("sub.f16x2 %0, %0, %1;" : "+r"(left[i]) : "r"(cut[i]));
                         }
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = __byte_perm(cut[8 * h + 2 * e], cut[8 * h + 2 * e + 1], 0x7531);
-                            *reinterpret_cast<uint4*>(p_row + (((2 * k + h) ^ (tid & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                        for (int e = 0; e < 4; ++e) v[e] = __byte_perm(cut[2 * e], cut[2 * e + 1], 0x7531);
+                        *reinterpret_cast<uint4*>(p_row + (((2 * k + wg) ^ (tid & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 } else {
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
+                    for (int h = 0; h < 2; ++h) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float a = w[8 * ch + 2 * e], b = w[8 * ch + 2 * e + 1];
+                            const float a = w[8 * h + 2 * e], b = w[8 * h + 2 * e + 1];
                             hi[e] = pack_bf16x2(a, b);
                             lo[e] = pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xFFFF0000u));
                         }
+                        const int ch = 2 * wg + h;
                         *reinterpret_cast<uint4*>(p_row + ((ch ^ (tid & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(p_row + (((4 + ch) ^ (tid & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(v + h * C::HALF + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int e = 4 * wg; e < 4 * wg + 4; ++e) *reinterpret_cast<uint4*>(v + h * C::HALF + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -419,22 +435,23 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
             // ------------------------------------------- the segment's result ---
             ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
             __syncwarp();
-            if (softmax_any(!ok)) {
+            if (softmax_any(wg, !ok)) {
                 dead = true;
                 break;
             }
             tc_fence_after();
-            float o[R];
+            float o[H];
 #pragma unroll
             for (int k = 0; k < C::TERMS; ++k) {
-                float y[R];
-                tmem_ld32f(tmem + lanes + C::O_COL + k * R, y);
+                float y[H];
+                tmem_ld16f(tmem + lanes + C::O_COL + k * R + first, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < R; ++r) o[r] = k ? o[r] + y[r] : y[r];
+                for (int i = 0; i < H; ++i) o[i] = k ? o[i] + y[i] : y[i];
             }
             tc_fence_before();
-            sm_red[warp][lane] = reduce32(l, [](float a, float b) { return a + b; });
+            const float sum_of = reduce16(l, [](float a, float b) { return a + b; });
+            red[w4][lane >> 1] = sum_of;
             // the keys that not every row sees, where the item ends
             const int tail = g.x1 == g.per_item ? g.seen_any - g.seen_all : 0;
             auto tail_factor = [&](int j, bool of_v) {
@@ -442,36 +459,37 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
                 const size_t at = ((size_t)x.b * p.nkb_max + j / p.B) * p.Hkv + hk;
                 return of_v ? p.vb_fac[at] : p.kb_fac[at];
             };
-            for (int i = tid; i < tail * R; i += 128) {
-                const int r = i % R, j = g.seen_all + i / R;
+            for (int i = tid; i < tail * H; i += 128) {
+                const int r = first + i % H, j = g.seen_all + i / H;
                 float z = -INFINITY;
                 if (r < g.rows && j <= s.P + token(r)) {
                     const long long row = key_row(p, s, x.b, j);
                     const float f = D.qk_scale * (FP8 ? p.k_scale[hk] * p.q_scale[head(r)] : 1.f) * tail_factor(j, false);
                     if (row >= 0) z = f * dot_row<FP8>(q_row(r), static_cast<const uint8_t*>(D.k) + (row * p.Hkv + hk) * RB);
                 }
-                sm_w[i / R][r] = z;
+                sm_w[i / H][r] = z;
             }
-            softmax_sync();
-            if (tid < R) {
-                const float m = -sm_nm[tid];
-                float most = m, sum = sm_red[0][tid] + sm_red[1][tid] + sm_red[2][tid] + sm_red[3][tid];
-                for (int k = 0; k < tail; ++k) most = fmaxf(most, sm_w[k][tid]);
+            softmax_sync(wg);
+            if (tid < H) {
+                const int r = first + tid;
+                const float m = -sm_nm[r];
+                float most = m, sum = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+                for (int k = 0; k < tail; ++k) most = fmaxf(most, sm_w[k][r]);
                 const float f = ex2(m - most);
                 sum *= f;
                 for (int k = 0; k < tail; ++k) {
-                    const float w = ex2(sm_w[k][tid] - most);
+                    const float w = ex2(sm_w[k][r] - most);
                     sum += w;
-                    sm_w[k][tid] = w * tail_factor(g.seen_all + k, true);
+                    sm_w[k][r] = w * tail_factor(g.seen_all + k, true);
                 }
-                sm_m[tid] = most;
-                sm_l[tid] = sum;
-                sm_f[tid] = f;
+                sm_m[r] = most;
+                sm_l[r] = sum;
+                sm_f[r] = f;
             }
-            softmax_sync();
+            softmax_sync(wg);
             if (tail > 0) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) o[r] *= sm_f[r];
+                for (int i = 0; i < H; ++i) o[i] *= sm_f[first + i];
                 for (int k = 0; k < tail; ++k) {
                     const int j = g.seen_all + k;
                     const long long row = key_row(p, s, x.b, j);
@@ -481,16 +499,17 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
                     if constexpr (FP8) v = e4m3_pair(static_cast<const uint8_t*>(D.v)[at]).x;
                     else v = __bfloat162float(static_cast<const __nv_bfloat16*>(D.v)[at]);
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (r < g.rows && j <= s.P + token(r)) o[r] = fmaf(sm_w[k][r], v, o[r]);
+                    for (int i = 0; i < H; ++i)
+                        if (first + i < g.rows && j <= s.P + token(first + i)) o[i] = fmaf(sm_w[k][first + i], v, o[i]);
                 }
             }
             const int slot = 2 * c + (g.x0 == 0 ? 1 : 0);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int i = 0; i < H; ++i) {
+                const int r = first + i;
                 if (r >= g.rows) break;
                 if (g.whole()) {
-                    const float y = o[r] * ((FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]);
+                    const float y = o[i] * ((FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]);
                     const long long at = ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * DH + tid;
                     if (p.out_fp8) {
                         const float unit = p.out_scale ? p.out_scale[head(r)] : p.v_scale[hk];
@@ -499,26 +518,27 @@ __global__ void __launch_bounds__(kTileThreads, Tile<FP8>::PER_SM)
                         static_cast<__nv_bfloat16*>(D.out)[at] = __float2bfloat16(y);
                     }
                 } else {
-                    D.part[(((size_t)slot * D.hc + hs) * R + r) * DH + tid] = o[r];
+                    D.part[(((size_t)slot * D.hc + hs) * R + r) * DH + tid] = o[i];
                 }
             }
-            if (tid < g.rows) {
+            if (tid < H && first + tid < g.rows) {
+                const int r = first + tid;
                 if (g.whole()) {
-                    if (D.lse) D.lse[(long long)(s.q0 + token(tid)) * p.Hq + head(tid)] = lse_of(sm_m[tid], sm_l[tid]);
+                    if (D.lse) D.lse[(long long)(s.q0 + token(r)) * p.Hq + head(r)] = lse_of(sm_m[r], sm_l[r]);
                 } else {
-                    const size_t at = ((size_t)slot * D.hc + hs) * R + tid;
-                    *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[tid], sm_l[tid]);
+                    const size_t at = ((size_t)slot * D.hc + hs) * R + r;
+                    *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[r], sm_l[r]);
                 }
             }
-            if (tid == 0 && hs == 0) put_record(D, x, g, c);
-            softmax_sync();  // sm_* are free for the next segment
+            if (threadIdx.x == 0 && hs == 0) put_record(D, x, g, c);
+            softmax_sync(wg);  // sm_* are free for the next segment
             x.u = g.item_at + g.x1;
         }
         if (dead && lane == 0) set_error(p.err, kErrTimeout, kDetTileSoftmax);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM);
     }
