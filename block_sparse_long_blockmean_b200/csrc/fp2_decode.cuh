@@ -19,7 +19,7 @@ constexpr int kDecBox = 16;                     // rows of a copy: they never cr
 constexpr float kLift = 7.f, kRoof = 15.f;
 
 struct DecodeMaps {
-    CUtensorMap k, v;  // [rows][Hkv][d], boxes of kDecBox rows x 128 bytes of one head
+    CUtensorMap k, v;  // [rows][Hkv][d], boxes of some rows x 128 bytes of one head
 };
 
 struct Shape {

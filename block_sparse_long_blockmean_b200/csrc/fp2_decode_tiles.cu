@@ -42,12 +42,13 @@ struct Tile {
     static constexpr int HALVES = RB / 128;               // 128-byte columns of a row
     static constexpr int HALF = kTileKeys * 128;          // bytes of one
     static constexpr int STAGE = 2 * HALVES * HALF;       // K, then V
-    static constexpr int STAGES = FP8 ? 6 : 3;
+    static constexpr int STAGES = FP8 ? 5 : 3;
+    static constexpr int P_BUFS = FP8 ? 2 : 1;            // weights' tiles
     static constexpr int TERMS = FP8 ? 4 : 2;             // operand terms of a weight
     static constexpr int PV_N = TERMS * kTileRows;        // columns of the second product: 128 bytes a key
     static constexpr int KSTEP = FP8 ? 32 : 16;           // k of one product
     static constexpr int OFF_P = STAGES * STAGE;
-    static constexpr int OFF_Q = OFF_P + HALF;
+    static constexpr int OFF_Q = OFF_P + P_BUFS * HALF;
     static constexpr int SMEM = OFF_Q + HALVES * kTileRows * 128;
     static constexpr int O_COL = 64;                      // TMEM: S twice, then O
     static constexpr uint32_t TMEM = FP8 ? 256 : 128;
@@ -55,7 +56,7 @@ struct Tile {
     static_assert(O_COL + PV_N <= (int)TMEM && SMEM <= 224 * 1024, "on-chip memory");
 };
 
-enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE, T_Q_READY, T_DRAIN, T_COUNT };
+enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_DRAIN, T_COUNT };
 enum { kDetTileCopy = kDetWaitBase + 8, kDetTileMma, kDetTileSoftmax };
 
 // Instruction descriptor with fp32 accumulation: operand formats a, b (kind::f16:
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
-            mbar_init(&bars[i], i == T_S_FREE || i == T_S_FREE + 1 || i == T_P_READY || i == T_Q_READY ? 256 : 1);
+            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY ? 256 : 1);
         fence_mbar_init();
         aborted = 0;
         prefetch_tmap(&maps.k);
@@ -179,10 +180,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         bool ok = true;
         while (ok && next_segment<R, kTileKeys>(D, x, g)) {
             const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
-            // lane 8 i + j: cache row of box j of tile 4 k + i, a round of 4 tiles ahead
+            // lane 8 i + j: cache row of box j of tile 4 k + i, a round of 4 tiles ahead;
+            // a box is a page, or a tile where pages are larger
             auto rows_of = [&](int n) {
-                const int tile = n + (lane >> 3), key = (g.x0 + tile) * kTileKeys + (lane & 7) * kDecBox;
-                return tile < n_tiles && key < g.seen_all ? (int)key_row(p, x.s, x.b, key) : -1;
+                const int tile = n + (lane >> 3), key = (g.x0 + tile) * kTileKeys + (lane & 7) * D.box;
+                return tile < n_tiles && (lane & 7) * D.box < kTileKeys && key < g.seen_all ? (int)key_row(p, x.s, x.b, key) : -1;
             };
             int now = rows_of(0), next = rows_of(4);
             for (int n = 0; n < n_tiles; ++n, ++t) {
@@ -199,10 +201,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 const bool mine = (lane >> 3) == (n & 3) && now >= 0;
                 const int boxes = __popc(__ballot_sync(~0u, mine));
-                if (lane == 0) mbar_arrive_expect_tx(&bars[T_FULL + st], boxes * kDecBox * RB * 2);
+                if (lane == 0) mbar_arrive_expect_tx(&bars[T_FULL + st], boxes * D.box * RB * 2);
                 __syncwarp();
                 if (mine) {
-                    const uint32_t dst = stage_of(t) + (lane & 7) * kDecBox * 128;
+                    const uint32_t dst = stage_of(t) + (lane & 7) * D.box * 128;
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h) {
                         tma_load_3d(dst + h * C::HALF, &maps.k, &bars[T_FULL + st], h * (FP8 ? 128 : 64), hk, now);
@@ -244,18 +246,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     if (n >= 1) {
                         const int i = t + n - 1;
-                        ok = mbar_wait(&bars[T_P_READY], i & 1, &aborted, kDecWaitNs);
+                        ok = mbar_wait(&bars[T_P_READY + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 0; ks < kTileKeys / C::KSTEP; ++ks) {  // KSTEP keys each
                             const uint64_t ad = sw128_desc(stage_of(i) + C::HALVES * C::HALF + ks * C::KSTEP * 128, C::HALF, 1024);
-                            const uint64_t bd = sw128_desc(base + C::OFF_P + ks * C::KSTEP * 128, C::HALF, 1024);
+                            const uint64_t bd = sw128_desc(base + C::OFF_P + i % C::P_BUFS * C::HALF + ks * C::KSTEP * 128, C::HALF, 1024);
                             const uint32_t acc = n > 1 || ks > 0;
                             if constexpr (FP8) mma_f8_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
                             else mma_bf16_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
                         }
-                        mma_commit(&bars[T_O_DONE]);
+                        mma_commit(&bars[T_O_DONE + (i & 1)]);
                         mma_commit(&bars[T_EMPTY + i % STAGES]);
                     }
                 }
@@ -275,7 +277,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int tid = threadIdx.x & 127;  // key of the tile, TMEM lane; d of the output
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         float(*const red)[H] = sm_red + 4 * wg;
-        uint8_t* const p_row = smem + C::OFF_P + tid * 128;
+        // the product of tile i has read its weights and values
+        auto product_done = [&](int i) { return mbar_wait(&bars[T_O_DONE + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs); };
         bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
         while (!dead && next_segment<R, kTileKeys>(D, x, g)) {
             const SeqInfo& s = x.s;
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                     for (int i = 0; i < H; ++i) l[i] *= sm_f[first + i];
                     if (n > 0) {
-                        ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
+                        ok = product_done(t - 1) && ok;
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
@@ -380,28 +383,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     w[i] = seen ? ex2(w[i]) : 0.f;
                     l[i] += w[i];
                 }
-                if (n > 0) {  // the product before has read P
-                    ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
-                    __syncwarp();
-                }
+                // the operand terms, 16 bytes of this warpgroup's rows per 32 columns
+                uint4 out[4];
+                int chunk[4];
                 if constexpr (FP8) {
                     uint32_t left[H / 2];  // fp16 pairs: what the terms so far leave
 #pragma unroll
                     for (int i = 0; i < H / 2; ++i) {
-                        const float f = p.kb_fac ? fac.y : 1.f;
-                        asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(left[i]) : "f"(w[2 * i] * f), "f"(w[2 * i + 1] * f));
+                        if (p.kb_fac) {
+                            w[2 * i] *= fac.y;
+                            w[2 * i + 1] *= fac.y;
+                        }
+                        asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(left[i]) : "f"(w[2 * i]), "f"(w[2 * i + 1]));
                     }
 #pragma unroll
-                    for (int k = 0; k < C::TERMS; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         uint32_t cut[H / 2], v[4];
 #pragma unroll
                         for (int i = 0; i < H / 2; ++i) {
                             cut[i] = left[i] & 0xFF00FF00u;
-                            if (k + 1 < C::TERMS) asm("sub.f16x2 %0, %0, %1;" : "+r"(left[i]) : "r"(cut[i]));
+                            if (k < 3) asm("sub.f16x2 %0, %0, %1;" : "+r"(left[i]) : "r"(cut[i]));
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] = __byte_perm(cut[2 * e], cut[2 * e + 1], 0x7531);
-                        *reinterpret_cast<uint4*>(p_row + (((2 * k + wg) ^ (tid & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        out[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                        chunk[k] = 2 * k + wg;
                     }
                 } else {
 #pragma unroll
@@ -413,11 +419,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             hi[e] = pack_bf16x2(a, b);
                             lo[e] = pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xFFFF0000u));
                         }
-                        const int ch = 2 * wg + h;
-                        *reinterpret_cast<uint4*>(p_row + ((ch ^ (tid & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(p_row + (((4 + ch) ^ (tid & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        out[h] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        out[2 + h] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        chunk[h] = 2 * wg + h;
+                        chunk[2 + h] = 4 + 2 * wg + h;
                     }
                 }
+                if (n >= C::P_BUFS) {  // the buffer's last reader
+                    ok = product_done(t - C::P_BUFS) && ok;
+                    __syncwarp();
+                }
+                uint8_t* const p_row = smem + C::OFF_P + t % C::P_BUFS * C::HALF + tid * 128;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
                 if (j0 + kTileKeys > g.seen_all && !seen) {
                     // rows of V that are none of these rows' values: finite
                     uint8_t* v = smem + (t % STAGES) * C::STAGE + C::HALVES * C::HALF + tid * 128;
@@ -428,12 +442,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&bars[T_P_READY]);
+                mbar_arrive(&bars[T_P_READY + (t & 1)]);
             }
             if (dead) break;
 
             // ------------------------------------------- the segment's result ---
-            ok = mbar_wait(&bars[T_O_DONE], (t - 1) & 1, &aborted, kDecWaitNs) && ok;
+            ok = product_done(t - 1) && ok;
             __syncwarp();
             if (softmax_any(wg, !ok)) {
                 dead = true;
@@ -545,14 +559,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 template <bool FP8>
-cudaError_t launch(const DecodeParams& D, cudaStream_t s) {
+cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using C = Tile<FP8>;
     static std::atomic<unsigned long long> ready{0};
     cudaError_t e = allow_smem(decode_tiles_kernel<FP8>, C::SMEM, ready);
     if (e != cudaSuccess) return e;
     DecodeMaps maps;
     const bool wide = D.hc * C::RB >= 256 || D.p.Hkv == 1;
-    if (!make_row_maps(D.p, D.k, D.v, kDecBox, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
+    D.box = D.p.paged && D.p.page_size < kTileKeys ? D.p.page_size : kTileKeys;
+    if (!make_row_maps(D.p, D.k, D.v, D.box, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
     return launch_early(decode_tiles_kernel<FP8>, dim3(C::CTAS), kTileThreads, C::SMEM, s, D, maps);
 }
 

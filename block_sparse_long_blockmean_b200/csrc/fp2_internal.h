@@ -120,6 +120,7 @@ struct DecodeParams {
     // set by the launcher: KV heads of an item, groups of them, row tiles of the
     // longest sequence, records by item (few items) or by share
     int hc, groups, tiles_max, few;
+    int box;                   // rows of a copy of the tile kernel
 };
 constexpr int kDecHeads = 2;   // most KV heads of an item
 constexpr int kDecCtas = 444;  // most CTAs of the split: 3 on each of 148 SMs
