@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __shared__ __align__(8) uint64_t bars[T_COUNT];
     __shared__ uint32_t tmem_at;
     __shared__ int aborted;
-    __shared__ float sm_red[8][kHalfRows], sm_m[R], sm_l[R], sm_f[R], sm_w[16][R], sm_sc[R], sm_nm[R];
+    __shared__ float sm_red[8][kHalfRows], sm_m[R], sm_l[R], sm_f[R], sm_w[16][R];
+    __shared__ __align__(16) float sm_sc[R], sm_nm[R];
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // adjacent CTAs take the heads of a group over the same keys, so that a token's
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
-            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY ? 256 : 1);
+            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY ? 8 : 1);
         fence_mbar_init();
         aborted = 0;
         prefetch_tmap(&maps.k);
@@ -277,6 +278,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int tid = threadIdx.x & 127;  // key of the tile, TMEM lane; d of the output
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         float(*const red)[H] = sm_red + 4 * wg;
+        // one arrival a warp: 32 on one barrier would queue
+        auto arrive = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         // the product of tile i has read its weights and values
         auto product_done = [&](int i) { return mbar_wait(&bars[T_O_DONE + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs); };
         bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * R * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bars[T_Q_READY]);
+            arrive(&bars[T_Q_READY]);
             float l[H];
 #pragma unroll
             for (int i = 0; i < H; ++i) l[i] = 0.f;
@@ -323,16 +329,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
                 tc_fence_after();
                 const bool seen = j0 + tid < g.seen_all;
+                const bool edge = j0 + kTileKeys > g.seen_all;  // some of the tile's keys are not seen
+                // the logits' factors and minus the references of rows 4 i .. 4 i + 3
+                auto exponents = [&](float (&w)[H]) {
+#pragma unroll
+                    for (int i = 0; i < H; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&sm_nm[first + i]);
+                        float4 f = make_float4(D.qk_scale, D.qk_scale, D.qk_scale, D.qk_scale);
+                        if constexpr (FP8) {
+                            f = *reinterpret_cast<const float4*>(&sm_sc[first + i]);
+                            if (p.kb_fac) f = scaled(f, fac.x);
+                        }
+                        const float2 a = ffma2(make_float2(w[i], w[i + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
+                        const float2 b = ffma2(make_float2(w[i + 2], w[i + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
+                        w[i] = a.x;
+                        w[i + 1] = a.y;
+                        w[i + 2] = b.x;
+                        w[i + 3] = b.y;
+                    }
+                };
                 auto factor = [&](int i) { return FP8 ? sm_sc[first + i] * fac.x : D.qk_scale; };
                 const uint32_t s_at = tmem + lanes + buf * R + first;
                 float w[H], top = -FLT_MAX;
                 tmem_ld16f(s_at, w);
                 tmem_wait_ld();
+                exponents(w);
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    w[i] = fmaf(w[i], factor(i), sm_nm[first + i]);
-                    top = fmaxf(top, w[i]);
-                }
+                for (int i = 0; i < H; i += 2) top = max3f(top, w[i], w[i + 1]);
                 if (softmax_any(wg, (seen && top > kRoof) || !ok)) {
                     if (softmax_any(wg, !ok)) {
                         dead = true;
@@ -373,15 +396,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     tmem_ld16f(s_at, w);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < H; ++i) w[i] = fmaf(w[i], factor(i), sm_nm[first + i]);
+                    exponents(w);
                 }
                 tc_fence_before();
-                mbar_arrive(&bars[T_S_FREE + buf]);
+                arrive(&bars[T_S_FREE + buf]);
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    w[i] = seen ? ex2(w[i]) : 0.f;
-                    l[i] += w[i];
+                for (int i = 0; i < H; ++i) w[i] = ex2(w[i]);
+                if (edge && !seen) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) w[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < H; i += 2) {
+                    const float2 x = fadd2(make_float2(l[i], l[i + 1]), make_float2(w[i], w[i + 1]));
+                    l[i] = x.x;
+                    l[i + 1] = x.y;
                 }
                 // the operand terms, 16 bytes of this warpgroup's rows per 32 columns
                 uint4 out[4];
@@ -432,7 +461,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 uint8_t* const p_row = smem + C::OFF_P + t % C::P_BUFS * C::HALF + tid * 128;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
-                if (j0 + kTileKeys > g.seen_all && !seen) {
+                if (edge && !seen) {
                     // rows of V that are none of these rows' values: finite
                     uint8_t* v = smem + (t % STAGES) * C::STAGE + C::HALVES * C::HALF + tid * 128;
 #pragma unroll
@@ -442,7 +471,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&bars[T_P_READY + (t & 1)]);
+                arrive(&bars[T_P_READY + (t & 1)]);
             }
             if (dead) break;
 
