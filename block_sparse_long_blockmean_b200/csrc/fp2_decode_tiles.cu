@@ -225,41 +225,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             constexpr uint32_t fmt = FP8 ? 0u : 1u;
             constexpr uint32_t idesc_qk = tile_idesc(fmt, fmt, false, R);
             constexpr uint32_t idesc_pv = tile_idesc(fmt, 1u, true, C::PV_N);  // e4m3 x e5m2, bf16 x bf16
+            // descriptors of the first stage; others differ in the address field (16 bytes a
+            // unit), which no sum below carries out of: one thread issues everything, so
+            // its own instructions count
+            const uint64_t dk = sw128_desc(base, 16, 1024), dq = sw128_desc(base + C::OFF_Q, 16, 1024);
+            const uint64_t dv = sw128_desc(base + C::HALVES * C::HALF, C::HALF, 1024), dp = sw128_desc(base + C::OFF_P, C::HALF, 1024);
             bool ok = true;
+            int k_stage = 0, k_phase = 0, v_stage = 0;
             for (int seg = 0; ok && next_segment<R, kTileKeys>(D, x, g); ++seg) {
                 const int n_tiles = g.x1 - g.x0;
                 ok = mbar_wait(&bars[T_Q_READY], seg & 1, &aborted, kDecWaitNs);
                 for (int n = 0; ok && n <= n_tiles; ++n) {
                     if (n < n_tiles) {
-                        const int i = t + n, st = i % STAGES, buf = i & 1;
-                        ok = mbar_wait(&bars[T_FULL + st], (i / STAGES) & 1, &aborted, kDecWaitNs) &&
+                        const int i = t + n, buf = i & 1;
+                        ok = mbar_wait(&bars[T_FULL + k_stage], k_phase, &aborted, kDecWaitNs) &&
                              (i < 2 || mbar_wait(&bars[T_S_FREE + buf], (i / 2 - 1) & 1, &aborted, kDecWaitNs));
                         if (!ok) break;
                         tc_fence_after();
+                        const uint64_t at = dk + (uint32_t)(k_stage * (C::STAGE >> 4));
 #pragma unroll
                         for (int ks = 0; ks < DH / C::KSTEP; ++ks) {  // 32 bytes of d each
-                            const uint64_t ad = sw128_desc(stage_of(i) + (ks >> 2) * C::HALF + (ks & 3) * 32, 16, 1024);
-                            const uint64_t bd = sw128_desc(base + C::OFF_Q + (ks >> 2) * R * 128 + (ks & 3) * 32, 16, 1024);
+                            const uint64_t ad = at + (uint32_t)((ks >> 2) * (C::HALF >> 4) + (ks & 3) * 2);
+                            const uint64_t bd = dq + (uint32_t)((ks >> 2) * (R * 128 >> 4) + (ks & 3) * 2);
                             if constexpr (FP8) mma_f8_ss(tmem + buf * R, ad, bd, idesc_qk, ks > 0);
                             else mma_bf16_ss(tmem + buf * R, ad, bd, idesc_qk, ks > 0);
                         }
                         mma_commit(&bars[T_S_FULL + buf]);
+                        if (++k_stage == STAGES) {
+                            k_stage = 0;
+                            k_phase ^= 1;
+                        }
                     }
                     if (n >= 1) {
                         const int i = t + n - 1;
                         ok = mbar_wait(&bars[T_P_READY + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs);
                         if (!ok) break;
                         tc_fence_after();
+                        const uint64_t at = dv + (uint32_t)(v_stage * (C::STAGE >> 4));
+                        const uint64_t bt = dp + (uint32_t)(i % C::P_BUFS * (C::HALF >> 4));
 #pragma unroll
                         for (int ks = 0; ks < kTileKeys / C::KSTEP; ++ks) {  // KSTEP keys each
-                            const uint64_t ad = sw128_desc(stage_of(i) + C::HALVES * C::HALF + ks * C::KSTEP * 128, C::HALF, 1024);
-                            const uint64_t bd = sw128_desc(base + C::OFF_P + i % C::P_BUFS * C::HALF + ks * C::KSTEP * 128, C::HALF, 1024);
+                            const uint64_t ad = at + (uint32_t)(ks * C::KSTEP * 8), bd = bt + (uint32_t)(ks * C::KSTEP * 8);
                             const uint32_t acc = n > 1 || ks > 0;
                             if constexpr (FP8) mma_f8_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
                             else mma_bf16_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
                         }
                         mma_commit(&bars[T_O_DONE + (i & 1)]);
-                        mma_commit(&bars[T_EMPTY + i % STAGES]);
+                        mma_commit(&bars[T_EMPTY + v_stage]);
+                        if (++v_stage == STAGES) v_stage = 0;
                     }
                 }
                 t += n_tiles;
