@@ -17,8 +17,9 @@
 // accumulators are added when the segment ends.
 //
 // Keys that only some of the tile's tokens see (at most 15, the new ones) stay out
-// of the tiles, where a weight of 0 would not keep a value that is not finite out
-// of the other rows' sums: they are added row by row when an item ends.
+// of the second product, where a weight of 0 would not keep a value that is not
+// finite out of the other rows' sums: their logits and values are set aside as their
+// tile passes, and added row by row when the segment ends.
 //
 // Warps 0-3 and 4-7: softmax of rows 0-15 and 16-31 (a thread a key); warp 8:
 // copies; warp 9: products.  They meet in mbarriers only, so that the copies run on
@@ -56,7 +57,7 @@ struct Tile {
     static_assert(O_COL + PV_N <= (int)TMEM && SMEM <= 224 * 1024, "on-chip memory");
 };
 
-enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_DRAIN, T_COUNT };
+enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_TAIL, T_DRAIN, T_COUNT };
 enum { kDetTileCopy = kDetWaitBase + 8, kDetTileMma, kDetTileSoftmax };
 
 // Instruction descriptor with fp32 accumulation: operand formats a, b (kind::f16:
@@ -114,28 +115,6 @@ __device__ __forceinline__ float2 e4m3_pair(uint16_t x) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
     return __half22float2(*reinterpret_cast<__half2*>(&y));
 }
-// q . k of one row each, in fp32.
-template <bool FP8>
-__device__ __forceinline__ float dot_row(const uint8_t* q, const uint8_t* k) {
-    float z = 0.f;
-    for (int i = 0; i < Tile<FP8>::RB; i += 16) {
-        const uint4 a = *reinterpret_cast<const uint4*>(q + i), b = *reinterpret_cast<const uint4*>(k + i);
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (FP8) {
-                const float2 a0 = e4m3_pair((uint16_t)x[e]), a1 = e4m3_pair((uint16_t)(x[e] >> 16));
-                const float2 b0 = e4m3_pair((uint16_t)y[e]), b1 = e4m3_pair((uint16_t)(y[e] >> 16));
-                z += a0.x * b0.x + a0.y * b0.y + a1.x * b1.x + a1.y * b1.y;
-            } else {
-                z += __uint_as_float(x[e] << 16) * __uint_as_float(y[e] << 16) +
-                     __uint_as_float(x[e] & 0xFFFF0000u) * __uint_as_float(y[e] & 0xFFFF0000u);
-            }
-        }
-    }
-    return z;
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(kTileThreads, 1)
     decode_tiles_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ DecodeMaps maps) {
@@ -145,7 +124,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __shared__ __align__(8) uint64_t bars[T_COUNT];
     __shared__ uint32_t tmem_at;
     __shared__ int aborted;
-    __shared__ float sm_red[8][kHalfRows], sm_m[R], sm_l[R], sm_f[R], sm_w[16][R];
+    __shared__ float sm_red[8][kHalfRows], sm_m[R], sm_l[R], sm_f[R];
+    // the keys that not every row sees: logits, then weights; value factors; values
+    __shared__ float sm_w[16][R], sm_tf[16];
+    __shared__ __align__(16) uint8_t sm_tv[16][RB];
     __shared__ __align__(16) float sm_sc[R], sm_nm[R];
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -155,7 +137,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
-            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY ? 8 : 1);
+            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY || i == T_TAIL ? 8 : 1);
         fence_mbar_init();
         aborted = 0;
         prefetch_tmap(&maps.k);
@@ -185,7 +167,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // a box is a page, or a tile where pages are larger
             auto rows_of = [&](int n) {
                 const int tile = n + (lane >> 3), key = (g.x0 + tile) * kTileKeys + (lane & 7) * D.box;
-                return tile < n_tiles && (lane & 7) * D.box < kTileKeys && key < g.seen_all ? (int)key_row(p, x.s, x.b, key) : -1;
+                return tile < n_tiles && (lane & 7) * D.box < kTileKeys && key < g.seen_any ? (int)key_row(p, x.s, x.b, key) : -1;
             };
             int now = rows_of(0), next = rows_of(4);
             for (int n = 0; n < n_tiles; ++n, ++t) {
@@ -299,6 +281,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // the product of tile i has read its weights and values
         auto product_done = [&](int i) { return mbar_wait(&bars[T_O_DONE + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs); };
         bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
+        int tails = 0;                 // segments with keys set aside
         while (!dead && next_segment<R, kTileKeys>(D, x, g)) {
             const SeqInfo& s = x.s;
             const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
@@ -411,6 +394,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     tmem_wait_ld();
                     exponents(w);
                 }
+                // a key of the tile that is set aside: its place among them
+                const int aside = j0 + tid < g.seen_any ? j0 + tid - g.seen_all : -1;
+                if (edge) {
+                    float z[H];
+                    tmem_ld16f(s_at, z);
+                    tmem_wait_ld();
+                    if (aside >= 0) {
+                        if (wg == 0) sm_tf[aside] = fac.y;
+#pragma unroll
+                        for (int i = 0; i < H; ++i)
+                            sm_w[aside][first + i] = j0 + tid <= s.P + token(first + i) ? z[i] * factor(i) : -INFINITY;
+                    }
+                }
                 tc_fence_before();
                 arrive(&bars[T_S_FREE + buf]);
 #pragma unroll
@@ -475,12 +471,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
                 if (edge && !seen) {
-                    // rows of V that are none of these rows' values: finite
+                    // rows of V that are not every row's values: set aside, then 0
                     uint8_t* v = smem + (t % STAGES) * C::STAGE + C::HALVES * C::HALF + tid * 128;
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-                        for (int e = 4 * wg; e < 4 * wg + 4; ++e) *reinterpret_cast<uint4*>(v + h * C::HALF + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int e = 4 * wg; e < 4 * wg + 4; ++e) {
+                            uint4* const at = reinterpret_cast<uint4*>(v + h * C::HALF + ((e ^ (tid & 7)) << 4));
+                            if (aside >= 0) *reinterpret_cast<uint4*>(&sm_tv[aside][h * 128 + e * 16]) = *at;
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                        }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -508,52 +508,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tc_fence_before();
             const float sum_of = reduce16(l, [](float a, float b) { return a + b; });
             red[w4][lane >> 1] = sum_of;
-            // the keys that not every row sees, where the item ends
-            const int tail = g.x1 == g.per_item ? g.seen_any - g.seen_all : 0;
-            auto tail_factor = [&](int j, bool of_v) {
-                if (!FP8 || !p.kb_fac) return 1.f;
-                const size_t at = ((size_t)x.b * p.nkb_max + j / p.B) * p.Hkv + hk;
-                return of_v ? p.vb_fac[at] : p.kb_fac[at];
-            };
-            for (int i = tid; i < tail * H; i += 128) {
-                const int r = first + i % H, j = g.seen_all + i / H;
-                float z = -INFINITY;
-                if (r < g.rows && j <= s.P + token(r)) {
-                    const long long row = key_row(p, s, x.b, j);
-                    const float f = D.qk_scale * (FP8 ? p.k_scale[hk] * p.q_scale[head(r)] : 1.f) * tail_factor(j, false);
-                    if (row >= 0) z = f * dot_row<FP8>(q_row(r), static_cast<const uint8_t*>(D.k) + (row * p.Hkv + hk) * RB);
-                }
-                sm_w[i / H][r] = z;
-            }
+            // the keys set aside in this segment: [from, to) of them
+            const int from = max(0, g.x0 * kTileKeys - g.seen_all);
+            const int to = min(g.seen_any, g.x1 * kTileKeys) - g.seen_all;
             softmax_sync(wg);
+            if (to > from) {  // (the other warpgroup holds half of the values)
+                arrive(&bars[T_TAIL]);
+                ok = mbar_wait(&bars[T_TAIL], tails & 1, &aborted, kDecWaitNs);
+                __syncwarp();
+                ++tails;
+                if (softmax_any(wg, !ok)) {
+                    dead = true;
+                    break;
+                }
+            }
             if (tid < H) {
                 const int r = first + tid;
                 const float m = -sm_nm[r];
                 float most = m, sum = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
-                for (int k = 0; k < tail; ++k) most = fmaxf(most, sm_w[k][r]);
+                for (int k = from; k < to; ++k) most = fmaxf(most, sm_w[k][r]);
                 const float f = ex2(m - most);
                 sum *= f;
-                for (int k = 0; k < tail; ++k) {
+                for (int k = from; k < to; ++k) {
                     const float w = ex2(sm_w[k][r] - most);
                     sum += w;
-                    sm_w[k][r] = w * tail_factor(g.seen_all + k, true);
+                    sm_w[k][r] = FP8 ? w * sm_tf[k] : w;
                 }
                 sm_m[r] = most;
                 sm_l[r] = sum;
                 sm_f[r] = f;
             }
             softmax_sync(wg);
-            if (tail > 0) {
+            if (to > from) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) o[i] *= sm_f[first + i];
-                for (int k = 0; k < tail; ++k) {
-                    const int j = g.seen_all + k;
-                    const long long row = key_row(p, s, x.b, j);
-                    if (row < 0) continue;
-                    const long long at = (row * p.Hkv + hk) * DH + tid;
+                for (int k = from; k < to; ++k) {
                     float v;
-                    if constexpr (FP8) v = e4m3_pair(static_cast<const uint8_t*>(D.v)[at]).x;
-                    else v = __bfloat162float(static_cast<const __nv_bfloat16*>(D.v)[at]);
+                    if constexpr (FP8) v = e4m3_pair(sm_tv[k][tid]).x;
+                    else v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sm_tv[k])[tid]);
+                    const int j = g.seen_all + k;
 #pragma unroll
                     for (int i = 0; i < H; ++i)
                         if (first + i < g.rows && j <= s.P + token(first + i)) o[i] = fmaf(sm_w[k][first + i], v, o[i]);
