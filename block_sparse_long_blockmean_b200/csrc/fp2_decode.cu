@@ -163,32 +163,33 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         const int first = x0 + warp / D.hc;
         const int steps = x1 > first ? (x1 - first + kw - 1) / kw : 0;
         // lane i: cache row where unit 32 k + i of this warp starts, and the
-        // unit's factors; loaded a round of 32 units ahead of their use
-        int row_now, row_next;
-        float2 fac_now, fac_next;
-        auto load_round = [&](int n0, int& row, float2& fac) {
-            const int x = first + (n0 + lane) * kw;
-            const bool on = x < x1;
-            row = on ? (int)key_row(p, s, b, x * kUnit) : -1;
-            fac = make_float2(1.f, 1.f);
-            if (FP8 && p.kb_fac && on) {
-                const size_t f = ((size_t)b * p.nkb_max + x * kUnit / p.B) * p.Hkv + hk;
-                fac = make_float2(p.kb_fac[f], p.vb_fac[f]);
-                if (!(fac.x > 0.f && fac.x <= 1.f && fac.y > 0.f && fac.y <= 1.f)) {
-                    set_error(p.err, kErrInvalid, kDetFactor);
-                    fac = make_float2(1.f, 1.f);
-                }
+        // unit's factors; the next round of 32 units is on its way, unchecked
+        int row_now = -1, raw_next = 0;
+        float2 fac_now = make_float2(1.f, 1.f), fac_next = fac_now;
+        auto key_at = [&](int n) { return (first + n * kw) * kUnit; };
+        auto fetch_round = [&](int n0) {
+            const int n = n0 + lane;
+            if (n >= steps) return;
+            raw_next = raw_row(p, s, b, key_at(n));
+            if (FP8 && p.kb_fac) {
+                const size_t f = ((size_t)b * p.nkb_max + key_at(n) / p.B) * p.Hkv + hk;
+                fac_next = make_float2(p.kb_fac[f], p.vb_fac[f]);
             }
         };
-        load_round(0, row_now, fac_now);
-        load_round(32, row_next, fac_next);
+        auto begin_round = [&](int n0) {
+            row_now = n0 + lane < steps ? checked_row(p, raw_next, key_at(n0 + lane)) : -1;
+            fac_now = fac_next;
+            if (FP8 && p.kb_fac && !(fac_now.x > 0.f && fac_now.x <= 1.f && fac_now.y > 0.f && fac_now.y <= 1.f)) {
+                set_error(p.err, kErrInvalid, kDetFactor);
+                fac_now = make_float2(1.f, 1.f);
+            }
+            fetch_round(n0 + 32);
+        };
+        fetch_round(0);
+        begin_round(0);
         auto issue = [&](int i, int stage) {
             if (i >= steps) return;
-            if (i > 0 && (i & 31) == 0) {
-                row_now = row_next;
-                fac_now = fac_next;
-                load_round(i + 32, row_next, fac_next);
-            }
+            if (i > 0 && (i & 31) == 0) begin_round(i);
             if (FP8 && p.kb_fac && lane == (i & 31)) sm_fac[warp][stage] = fac_now;
             const int row0 = __shfl_sync(~0u, row_now, i & 31);
             if (lane == 0) {

@@ -47,6 +47,20 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return a / b;
 }
 
+// Cache row of key `key` in two steps, so that a page id can be on its way while
+// other work is done: what has to be loaded, and the row, -1 (recorded) if it is bad.
+__device__ __forceinline__ int raw_row(const KParams& p, const SeqInfo& s, int b, int key) {
+    return p.paged ? p.page_table[(size_t)b * p.max_pages + key / p.page_size] : s.k0 + key;
+}
+__device__ __forceinline__ int checked_row(const KParams& p, int raw, int key) {
+    if (!p.paged) return raw;
+    if (raw < 0 || raw >= p.num_pages) {
+        set_error(p.err, kErrBounds, kDetPage);
+        return -1;
+    }
+    return raw * p.page_size + key % p.page_size;
+}
+
 // Sum of x over the CTA of W warps and the exclusive prefix of the calling thread.
 template <int W>
 __device__ __forceinline__ long long block_prefix(long long x, long long& total, long long* sums) {

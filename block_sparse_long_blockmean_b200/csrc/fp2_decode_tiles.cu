@@ -163,17 +163,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         bool ok = true;
         while (ok && next_segment<R, kTileKeys>(D, x, g)) {
             const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
-            // lane 8 i + j: cache row of box j of tile 4 k + i, a round of 4 tiles ahead;
-            // a box is a page, or a tile where pages are larger
-            auto rows_of = [&](int n) {
-                const int tile = n + (lane >> 3), key = (g.x0 + tile) * kTileKeys + (lane & 7) * D.box;
-                return tile < n_tiles && (lane & 7) * D.box < kTileKeys && key < g.seen_any ? (int)key_row(p, x.s, x.b, key) : -1;
+            // lane 8 i + j: cache row of box j of tile 4 k + i, the next round of 4 tiles on
+            // its way, unchecked; a box is a page, or a tile where pages are larger
+            const int lane_key = (lane >> 3) * kTileKeys + (lane & 7) * D.box;
+            auto key_of = [&](int n) { return (g.x0 + n) * kTileKeys + lane_key; };
+            auto wanted = [&](int n) {
+                return n + (lane >> 3) < n_tiles && (lane & 7) * D.box < kTileKeys && key_of(n) < g.seen_any;
             };
-            int now = rows_of(0), next = rows_of(4);
+            int now = -1, next = wanted(0) ? raw_row(p, x.s, x.b, key_of(0)) : 0;
             for (int n = 0; n < n_tiles; ++n, ++t) {
-                if (n > 0 && (n & 3) == 0) {
-                    now = next;
-                    next = rows_of(n + 4);
+                if ((n & 3) == 0) {
+                    now = wanted(n) ? checked_row(p, next, key_of(n)) : -1;
+                    if (wanted(n + 4)) next = raw_row(p, x.s, x.b, key_of(n + 4));
                 }
                 const int st = t % STAGES;
                 if (t >= STAGES &&
