@@ -6,7 +6,7 @@
 //   S^T (128 keys x 32 rows)  = K (128 x d) Q^T           both K-major
 //   O^T (128 d x 32 rows)    += V^T (d x 128 keys) P^T    both MN-major, as stored
 // so that neither K nor V is transposed or converted; a thread owns one key's
-// logits of 16 rows and, at the end, one d of their outputs.
+// logits and, at the end, one d of the outputs.
 //
 // The weights P need more than one 8-bit (or bf16) operand to keep their
 // precision.  e4m3 caches: w is rounded to fp16 (11 bits) and cut into four e5m2
@@ -21,8 +21,8 @@
 // finite out of the other rows' sums: their logits and values are set aside as their
 // tile passes, and added row by row when the segment ends.
 //
-// Warps 0-3 and 4-7: softmax of rows 0-15 and 16-31 (a thread a key); warp 8:
-// copies; warp 9: products.  They meet in mbarriers only, so that the copies run on
+// Warpgroups of four warps take the softmax, a thread a key; one more warp copies,
+// one issues the products.  They meet in mbarriers only, so that the copies run on
 // into the next segment.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,8 +33,7 @@ namespace fp2 {
 
 namespace {
 
-constexpr int kTileKeys = 128, kTileRows = 32, kTileWarps = 10, kTileThreads = 32 * kTileWarps;
-constexpr int kHalfRows = kTileRows / 2;  // of a softmax warpgroup
+constexpr int kTileKeys = 128, kTileRows = 32;
 
 template <bool FP8>
 struct Tile {
@@ -43,8 +42,14 @@ struct Tile {
     static constexpr int HALVES = RB / 128;               // 128-byte columns of a row
     static constexpr int HALF = kTileKeys * 128;          // bytes of one
     static constexpr int STAGE = 2 * HALVES * HALF;       // K, then V
-    static constexpr int STAGES = FP8 ? 5 : 3;
-    static constexpr int P_BUFS = FP8 ? 2 : 1;            // weights' tiles
+    // e4m3 tiles arrive faster than a warpgroup takes their softmax: two CTAs on each
+    // SM.  bf16 stages leave room for one, whose rows two warpgroups share.
+    static constexpr int PER_SM = FP8 ? 2 : 1;
+    static constexpr int WGS = FP8 ? 1 : 2;               // softmax warpgroups
+    static constexpr int H = kTileRows / WGS;             // rows of one
+    static constexpr int WARPS = 4 * WGS + 2, THREADS = 32 * WARPS;
+    static constexpr int STAGES = FP8 ? 2 : 3;
+    static constexpr int P_BUFS = 1;                      // weights' tiles
     static constexpr int TERMS = FP8 ? 4 : 2;             // operand terms of a weight
     static constexpr int PV_N = TERMS * kTileRows;        // columns of the second product: 128 bytes a key
     static constexpr int KSTEP = FP8 ? 32 : 16;           // k of one product
@@ -53,8 +58,8 @@ struct Tile {
     static constexpr int SMEM = OFF_Q + HALVES * kTileRows * 128;
     static constexpr int O_COL = 64;                      // TMEM: S twice, then O
     static constexpr uint32_t TMEM = FP8 ? 256 : 128;
-    static constexpr int CTAS = 148;                      // one on each SM
-    static_assert(O_COL + PV_N <= (int)TMEM && SMEM <= 224 * 1024, "on-chip memory");
+    static constexpr int CTAS = 148 * PER_SM;
+    static_assert(O_COL + PV_N <= (int)TMEM && PER_SM * (SMEM + 9 * 1024) <= 228 * 1024, "on-chip memory");
 };
 
 enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_TAIL, T_DRAIN, T_COUNT };
@@ -78,36 +83,44 @@ __device__ __forceinline__ bool softmax_any(int wg, bool x) {
     return r != 0;
 }
 
-// Lanes 2 i and 2 i + 1 get the reduction of v[i] over the warp's lanes.
-template <typename Op>
-__device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
+// The reduction of v[i] over the warp's lanes: in lane i of 32 rows, in lanes 2 i
+// and 2 i + 1 of 16.
+template <int H, typename Op>
+__device__ __forceinline__ float reduce_rows(float (&v)[H], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int half = 8; half > 0; half >>= 1) {
-        const bool up = lane & (2 * half);
+    for (int half = H / 2; half > 0; half >>= 1) {
+        const int mask = half * (32 / H);
+        const bool up = lane & mask;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(~0u, send, 2 * half));
+            v[i] = op(keep, __shfl_xor_sync(~0u, send, mask));
         }
     }
-    return op(v[0], __shfl_xor_sync(~0u, v[0], 1));
+    return H == 32 ? v[0] : op(v[0], __shfl_xor_sync(~0u, v[0], 1));
 }
 
 // 32 lanes x 16 consecutive 32-bit TMEM columns.
-__device__ __forceinline__ void tmem_ld16f(uint32_t at, float (&f)[16]) {
+__device__ __forceinline__ void tmem_ld16f(uint32_t at, float* f) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]),
           "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
         : "r"(at));
 }
-__device__ __forceinline__ void tmem_st16f(uint32_t at, const float (&f)[16]) {
+__device__ __forceinline__ void tmem_st16f(uint32_t at, const float* f) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
         "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "f"(f[8]), "f"(f[9]), "f"(f[10]),
         "f"(f[11]), "f"(f[12]), "f"(f[13]), "f"(f[14]), "f"(f[15])
         : "memory");
+}
+template <int H>
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&f)[H]) {
+    if constexpr (H == 32) tmem_ld32f(at, f);
+    else tmem_ld16f(at, f);
+    tmem_wait_ld();
 }
 
 __device__ __forceinline__ float2 e4m3_pair(uint16_t x) {
@@ -116,15 +129,16 @@ __device__ __forceinline__ float2 e4m3_pair(uint16_t x) {
     return __half22float2(*reinterpret_cast<__half2*>(&y));
 }
 template <bool FP8>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     decode_tiles_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ DecodeMaps maps) {
     using C = Tile<FP8>;
-    constexpr int R = kTileRows, DH = C::DH, RB = C::RB, STAGES = C::STAGES;
+    constexpr int R = kTileRows, H = C::H, WGS = C::WGS, DH = C::DH, RB = C::RB, STAGES = C::STAGES;
+    constexpr int COPY_WARP = 4 * WGS, MMA_WARP = COPY_WARP + 1;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[T_COUNT];
     __shared__ uint32_t tmem_at;
     __shared__ int aborted;
-    __shared__ float sm_red[8][kHalfRows], sm_m[R], sm_l[R], sm_f[R];
+    __shared__ float sm_red[4 * WGS][H], sm_m[R], sm_l[R], sm_f[R];
     // the keys that not every row sees: logits, then weights; value factors; values
     __shared__ float sm_w[16][R], sm_tf[16];
     __shared__ __align__(16) uint8_t sm_tv[16][RB];
@@ -137,7 +151,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
-            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY || i == T_TAIL ? 8 : 1);
+            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY || i == T_TAIL ? 4 * WGS : 1);
         fence_mbar_init();
         aborted = 0;
         prefetch_tmap(&maps.k);
@@ -145,8 +159,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     wait_previous();
     Share x;
-    if (!find_share<R, kTileKeys, kTileWarps>(D, c, gridDim.x / D.hc, 1, hs == 0, x)) return;
-    if (warp == 9) {
+    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.x / D.hc, 1, hs == 0, x)) return;
+    if (warp == MMA_WARP) {
         tmem_alloc(&tmem_at, C::TMEM);
         tmem_relinquish();
     }
@@ -158,7 +172,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int t = 0;  // tiles before the present one, over all segments: stages and phases follow it
     auto stage_of = [&](int i) { return base + (i % STAGES) * C::STAGE; };
 
-    if (warp == 8) {
+    if (warp == COPY_WARP) {
         // ------------------------------------------------------------ copies ---
         bool ok = true;
         while (ok && next_segment<R, kTileKeys>(D, x, g)) {
@@ -202,7 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int ignore = 0;
         for (int i = max(0, t - STAGES); i < t; ++i)
             mbar_wait(&bars[T_FULL + i % STAGES], (i / STAGES) & 1, &ignore, kDecWaitNs);
-    } else if (warp == 9) {
+    } else if (warp == MMA_WARP) {
         // ---------------------------------------------------------- products ---
         if (lane == 0) {
             constexpr uint32_t fmt = FP8 ? 0u : 1u;
@@ -269,8 +283,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
     } else {
         // ----------------------------------------------------------- softmax ---
-        constexpr int H = kHalfRows;
-        const int wg = warp >> 2, w4 = warp & 3, first = wg * H;  // rows first + 0 .. H - 1
+        const int wg = warp >> 2, w4 = warp & 3, first = wg * H;  // rows first .. first + H - 1
         const int tid = threadIdx.x & 127;  // key of the tile, TMEM lane; d of the output
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         float(*const red)[H] = sm_red + 4 * wg;
@@ -348,8 +361,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 auto factor = [&](int i) { return FP8 ? sm_sc[first + i] * fac.x : D.qk_scale; };
                 const uint32_t s_at = tmem + lanes + buf * R + first;
                 float w[H], top = -FLT_MAX;
-                tmem_ld16f(s_at, w);
-                tmem_wait_ld();
+                tmem_load(s_at, w);
                 exponents(w);
 #pragma unroll
                 for (int i = 0; i < H; i += 2) top = max3f(top, w[i], w[i + 1]);
@@ -359,12 +371,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         break;
                     }
                     // the references move: each row's largest z over the tile's keys
-                    tmem_ld16f(s_at, w);
-                    tmem_wait_ld();
+                    tmem_load(s_at, w);
 #pragma unroll
                     for (int i = 0; i < H; ++i) w[i] = seen ? w[i] * factor(i) : -INFINITY;
-                    const float top_of = reduce16(w, [](float a, float b) { return fmaxf(a, b); });
-                    red[w4][lane >> 1] = top_of;
+                    const float top_of = reduce_rows<H>(w, [](float a, float b) { return fmaxf(a, b); });
+                    red[w4][H == 32 ? lane : lane >> 1] = top_of;
                     softmax_sync(wg);
                     if (tid < H) {
                         const float most = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
@@ -383,24 +394,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
                         for (int k = 0; k < C::TERMS; ++k) {
                             const uint32_t o_at = tmem + lanes + C::O_COL + k * R + first;
-                            tmem_ld16f(o_at, w);
-                            tmem_wait_ld();
+                            tmem_load(o_at, w);
 #pragma unroll
                             for (int i = 0; i < H; ++i) w[i] *= sm_f[first + i];
-                            tmem_st16f(o_at, w);
+#pragma unroll
+                            for (int i = 0; i < H; i += 16) tmem_st16f(o_at + i, w + i);
                         }
                         tmem_wait_st();
                     }
-                    tmem_ld16f(s_at, w);
-                    tmem_wait_ld();
+                    tmem_load(s_at, w);
                     exponents(w);
                 }
                 // a key of the tile that is set aside: its place among them
                 const int aside = j0 + tid < g.seen_any ? j0 + tid - g.seen_all : -1;
                 if (edge) {
                     float z[H];
-                    tmem_ld16f(s_at, z);
-                    tmem_wait_ld();
+                    tmem_load(s_at, z);
                     if (aside >= 0) {
                         if (wg == 0) sm_tf[aside] = fac.y;
 #pragma unroll
@@ -422,9 +431,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     l[i] = x.x;
                     l[i + 1] = x.y;
                 }
-                // the operand terms, 16 bytes of this warpgroup's rows per 32 columns
-                uint4 out[4];
-                int chunk[4];
+                // the operand terms: columns 32 k + row of the key's 128 bytes of P
+                uint4 out[4 * H / 16];
+                int chunk[4 * H / 16];
                 if constexpr (FP8) {
                     uint32_t left[H / 2];  // fp16 pairs: what the terms so far leave
 #pragma unroll
@@ -437,20 +446,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        uint32_t cut[H / 2], v[4];
+                        uint32_t cut[H / 2];
 #pragma unroll
                         for (int i = 0; i < H / 2; ++i) {
                             cut[i] = left[i] & 0xFF00FF00u;
                             if (k < 3) asm("sub.f16x2 %0, %0, %1;" : "+r"(left[i]) : "r"(cut[i]));
                         }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = __byte_perm(cut[2 * e], cut[2 * e + 1], 0x7531);
-                        out[k] = make_uint4(v[0], v[1], v[2], v[3]);
-                        chunk[k] = 2 * k + wg;
+                        for (int h = 0; h < H / 16; ++h) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = __byte_perm(cut[8 * h + 2 * e], cut[8 * h + 2 * e + 1], 0x7531);
+                            out[k * (H / 16) + h] = make_uint4(v[0], v[1], v[2], v[3]);
+                            chunk[k * (H / 16) + h] = 2 * k + first / 16 + h;
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < H / 8; ++h) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -458,10 +471,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             hi[e] = pack_bf16x2(a, b);
                             lo[e] = pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xFFFF0000u));
                         }
-                        out[h] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        out[2 + h] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        chunk[h] = 2 * wg + h;
-                        chunk[2 + h] = 4 + 2 * wg + h;
+                        out[2 * h] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        out[2 * h + 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        chunk[2 * h] = first / 8 + h;
+                        chunk[2 * h + 1] = 4 + first / 8 + h;
                     }
                 }
                 if (n >= C::P_BUFS) {  // the buffer's last reader
@@ -470,14 +483,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 uint8_t* const p_row = smem + C::OFF_P + t % C::P_BUFS * C::HALF + tid * 128;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
+                for (int k = 0; k < 4 * H / 16; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
                 if (edge && !seen) {
                     // rows of V that are not every row's values: set aside, then 0
                     uint8_t* v = smem + (t % STAGES) * C::STAGE + C::HALVES * C::HALF + tid * 128;
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-                        for (int e = 4 * wg; e < 4 * wg + 4; ++e) {
+                        for (int e = wg * (8 / WGS); e < (wg + 1) * (8 / WGS); ++e) {
                             uint4* const at = reinterpret_cast<uint4*>(v + h * C::HALF + ((e ^ (tid & 7)) << 4));
                             if (aside >= 0) *reinterpret_cast<uint4*>(&sm_tv[aside][h * 128 + e * 16]) = *at;
                             *at = make_uint4(0u, 0u, 0u, 0u);
@@ -501,19 +514,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int k = 0; k < C::TERMS; ++k) {
                 float y[H];
-                tmem_ld16f(tmem + lanes + C::O_COL + k * R + first, y);
-                tmem_wait_ld();
+                tmem_load(tmem + lanes + C::O_COL + k * R + first, y);
 #pragma unroll
                 for (int i = 0; i < H; ++i) o[i] = k ? o[i] + y[i] : y[i];
             }
             tc_fence_before();
-            const float sum_of = reduce16(l, [](float a, float b) { return a + b; });
-            red[w4][lane >> 1] = sum_of;
+            const float sum_of = reduce_rows<H>(l, [](float a, float b) { return a + b; });
+            red[w4][H == 32 ? lane : lane >> 1] = sum_of;
             // the keys set aside in this segment: [from, to) of them
             const int from = max(0, g.x0 * kTileKeys - g.seen_all);
             const int to = min(g.seen_any, g.x1 * kTileKeys) - g.seen_all;
             softmax_sync(wg);
-            if (to > from) {  // (the other warpgroup holds half of the values)
+            if (WGS > 1 && to > from) {  // (the other warpgroup holds half of the values)
                 arrive(&bars[T_TAIL]);
                 ok = mbar_wait(&bars[T_TAIL], tails & 1, &aborted, kDecWaitNs);
                 __syncwarp();
@@ -588,7 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM);
     }
@@ -604,7 +616,7 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     const bool wide = D.hc * C::RB >= 256 || D.p.Hkv == 1;
     D.box = D.p.paged && D.p.page_size < kTileKeys ? D.p.page_size : kTileKeys;
     if (!make_row_maps(D.p, D.k, D.v, D.box, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
-    return launch_early(decode_tiles_kernel<FP8>, dim3(C::CTAS), kTileThreads, C::SMEM, s, D, maps);
+    return launch_early(decode_tiles_kernel<FP8>, dim3(C::CTAS), C::THREADS, C::SMEM, s, D, maps);
 }
 
 }  // namespace
