@@ -41,19 +41,21 @@ struct Tile {
     static constexpr int RB = DH * (FP8 ? 1 : 2);
     static constexpr int HALVES = RB / 128;               // 128-byte columns of a row
     static constexpr int HALF = kTileKeys * 128;          // bytes of one
-    static constexpr int STAGE = 2 * HALVES * HALF;       // K, then V
+    static constexpr int STAGE = HALVES * HALF;           // a tile of K or of V
     // e4m3 tiles arrive faster than a warpgroup takes their softmax: two CTAs on each
     // SM.  bf16 stages leave room for one, whose rows two warpgroups share.
     static constexpr int PER_SM = FP8 ? 2 : 1;
     static constexpr int WGS = FP8 ? 1 : 2;               // softmax warpgroups
     static constexpr int H = kTileRows / WGS;             // rows of one
     static constexpr int WARPS = 4 * WGS + 2, THREADS = 32 * WARPS;
-    static constexpr int STAGES = FP8 ? 2 : 3;
+    // K is free once its logits are there, V only after its product
+    static constexpr int K_STAGES = FP8 ? 2 : 3, V_STAGES = 3;
     static constexpr int P_BUFS = 1;                      // weights' tiles
     static constexpr int TERMS = FP8 ? 4 : 2;             // operand terms of a weight
     static constexpr int PV_N = TERMS * kTileRows;        // columns of the second product: 128 bytes a key
     static constexpr int KSTEP = FP8 ? 32 : 16;           // k of one product
-    static constexpr int OFF_P = STAGES * STAGE;
+    static constexpr int OFF_V = K_STAGES * STAGE;
+    static constexpr int OFF_P = OFF_V + V_STAGES * STAGE;
     static constexpr int OFF_Q = OFF_P + P_BUFS * HALF;
     static constexpr int SMEM = OFF_Q + HALVES * kTileRows * 128;
     static constexpr int O_COL = 64;                      // TMEM: S twice, then O
@@ -62,7 +64,7 @@ struct Tile {
     static_assert(O_COL + PV_N <= (int)TMEM && PER_SM * (SMEM + 9 * 1024) <= 228 * 1024, "on-chip memory");
 };
 
-enum { T_FULL = 0, T_EMPTY = 6, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_TAIL, T_DRAIN, T_COUNT };
+enum { T_K_FULL = 0, T_K_EMPTY = 3, T_V_FULL = 6, T_V_EMPTY = 9, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_TAIL, T_DRAIN, T_COUNT };
 enum { kDetTileCopy = kDetWaitBase + 8, kDetTileMma, kDetTileSoftmax };
 
 // Instruction descriptor with fp32 accumulation: operand formats a, b (kind::f16:
@@ -132,7 +134,7 @@ template <bool FP8>
 __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     decode_tiles_kernel(const __grid_constant__ DecodeParams D, const __grid_constant__ DecodeMaps maps) {
     using C = Tile<FP8>;
-    constexpr int R = kTileRows, H = C::H, WGS = C::WGS, DH = C::DH, RB = C::RB, STAGES = C::STAGES;
+    constexpr int R = kTileRows, H = C::H, WGS = C::WGS, DH = C::DH, RB = C::RB;
     constexpr int COPY_WARP = 4 * WGS, MMA_WARP = COPY_WARP + 1;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[T_COUNT];
@@ -170,11 +172,11 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     const uint32_t tmem = tmem_at;
     Segment g;
     int t = 0;  // tiles before the present one, over all segments: stages and phases follow it
-    auto stage_of = [&](int i) { return base + (i % STAGES) * C::STAGE; };
 
     if (warp == COPY_WARP) {
         // ------------------------------------------------------------ copies ---
         bool ok = true;
+        int k_copies = 0;  // t, or one more if V's copy failed
         while (ok && next_segment<R, kTileKeys>(D, x, g)) {
             const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
             // lane 8 i + j: cache row of box j of tile 4 k + i, the next round of 4 tiles on
@@ -190,32 +192,41 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     now = wanted(n) ? checked_row(p, next, key_of(n)) : -1;
                     if (wanted(n + 4)) next = raw_row(p, x.s, x.b, key_of(n + 4));
                 }
-                const int st = t % STAGES;
-                if (t >= STAGES &&
-                    !__all_sync(~0u, mbar_wait(&bars[T_EMPTY + st], (t / STAGES - 1) & 1, &aborted, kDecWaitNs))) {
-                    if (lane == 0) set_error(p.err, kErrTimeout, kDetTileCopy);
-                    ok = false;
-                    break;
-                }
                 const bool mine = (lane >> 3) == (n & 3) && now >= 0;
-                const int boxes = __popc(__ballot_sync(~0u, mine));
-                if (lane == 0) mbar_arrive_expect_tx(&bars[T_FULL + st], boxes * D.box * RB * 2);
-                __syncwarp();
-                if (mine) {
-                    const uint32_t dst = stage_of(t) + (lane & 7) * D.box * 128;
+                const int bytes = __popc(__ballot_sync(~0u, mine)) * D.box * RB;
+                // one of the tile's operands into its ring
+                auto copy = [&](const CUtensorMap* map, int stages, int offset, int full, int empty) {
+                    const int st = t % stages;
+                    if (t >= stages && !__all_sync(~0u, mbar_wait(&bars[empty + st], (t / stages - 1) & 1, &aborted, kDecWaitNs)))
+                        return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[full + st], bytes);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t dst = base + offset + st * C::STAGE + (lane & 7) * D.box * 128;
 #pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h) {
-                        tma_load_3d(dst + h * C::HALF, &maps.k, &bars[T_FULL + st], h * (FP8 ? 128 : 64), hk, now);
-                        tma_load_3d(dst + (C::HALVES + h) * C::HALF, &maps.v, &bars[T_FULL + st], h * (FP8 ? 128 : 64), hk, now);
+                        for (int h = 0; h < C::HALVES; ++h)
+                            tma_load_3d(dst + h * C::HALF, map, &bars[full + st], h * (FP8 ? 128 : 64), hk, now);
                     }
+                    return true;
+                };
+                ok = copy(&maps.k, C::K_STAGES, 0, T_K_FULL, T_K_EMPTY);
+                if (ok) {
+                    ++k_copies;
+                    ok = copy(&maps.v, C::V_STAGES, C::OFF_V, T_V_FULL, T_V_EMPTY);
+                }
+                if (!ok) {
+                    if (lane == 0) set_error(p.err, kErrTimeout, kDetTileCopy);
+                    break;
                 }
             }
             x.u = g.item_at + g.x1;
         }
         // never leave with copies in flight
         int ignore = 0;
-        for (int i = max(0, t - STAGES); i < t; ++i)
-            mbar_wait(&bars[T_FULL + i % STAGES], (i / STAGES) & 1, &ignore, kDecWaitNs);
+        for (int i = max(0, k_copies - C::K_STAGES); i < k_copies; ++i)
+            mbar_wait(&bars[T_K_FULL + i % C::K_STAGES], (i / C::K_STAGES) & 1, &ignore, kDecWaitNs);
+        for (int i = max(0, t - C::V_STAGES); i < t; ++i)
+            mbar_wait(&bars[T_V_FULL + i % C::V_STAGES], (i / C::V_STAGES) & 1, &ignore, kDecWaitNs);
     } else if (warp == MMA_WARP) {
         // ---------------------------------------------------------- products ---
         if (lane == 0) {
@@ -226,16 +237,16 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             // unit), which no sum below carries out of: one thread issues everything, so
             // its own instructions count
             const uint64_t dk = sw128_desc(base, 16, 1024), dq = sw128_desc(base + C::OFF_Q, 16, 1024);
-            const uint64_t dv = sw128_desc(base + C::HALVES * C::HALF, C::HALF, 1024), dp = sw128_desc(base + C::OFF_P, C::HALF, 1024);
+            const uint64_t dv = sw128_desc(base + C::OFF_V, C::HALF, 1024), dp = sw128_desc(base + C::OFF_P, C::HALF, 1024);
             bool ok = true;
-            int k_stage = 0, k_phase = 0, v_stage = 0;
+            int k_stage = 0, k_phase = 0, v_stage = 0, v_phase = 0;
             for (int seg = 0; ok && next_segment<R, kTileKeys>(D, x, g); ++seg) {
                 const int n_tiles = g.x1 - g.x0;
                 ok = mbar_wait(&bars[T_Q_READY], seg & 1, &aborted, kDecWaitNs);
                 for (int n = 0; ok && n <= n_tiles; ++n) {
                     if (n < n_tiles) {
                         const int i = t + n, buf = i & 1;
-                        ok = mbar_wait(&bars[T_FULL + k_stage], k_phase, &aborted, kDecWaitNs) &&
+                        ok = mbar_wait(&bars[T_K_FULL + k_stage], k_phase, &aborted, kDecWaitNs) &&
                              (i < 2 || mbar_wait(&bars[T_S_FREE + buf], (i / 2 - 1) & 1, &aborted, kDecWaitNs));
                         if (!ok) break;
                         tc_fence_after();
@@ -248,14 +259,16 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                             else mma_bf16_ss(tmem + buf * R, ad, bd, idesc_qk, ks > 0);
                         }
                         mma_commit(&bars[T_S_FULL + buf]);
-                        if (++k_stage == STAGES) {
+                        mma_commit(&bars[T_K_EMPTY + k_stage]);
+                        if (++k_stage == C::K_STAGES) {
                             k_stage = 0;
                             k_phase ^= 1;
                         }
                     }
                     if (n >= 1) {
                         const int i = t + n - 1;
-                        ok = mbar_wait(&bars[T_P_READY + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs);
+                        ok = mbar_wait(&bars[T_V_FULL + v_stage], v_phase, &aborted, kDecWaitNs) &&
+                             mbar_wait(&bars[T_P_READY + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t at = dv + (uint32_t)(v_stage * (C::STAGE >> 4));
@@ -268,8 +281,11 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                             else mma_bf16_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
                         }
                         mma_commit(&bars[T_O_DONE + (i & 1)]);
-                        mma_commit(&bars[T_EMPTY + v_stage]);
-                        if (++v_stage == STAGES) v_stage = 0;
+                        mma_commit(&bars[T_V_EMPTY + v_stage]);
+                        if (++v_stage == C::V_STAGES) {
+                            v_stage = 0;
+                            v_phase ^= 1;
+                        }
                     }
                 }
                 t += n_tiles;
@@ -484,9 +500,13 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                 uint8_t* const p_row = smem + C::OFF_P + t % C::P_BUFS * C::HALF + tid * 128;
 #pragma unroll
                 for (int k = 0; k < 4 * H / 16; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
+                if (edge) {
+                    ok = mbar_wait(&bars[T_V_FULL + t % C::V_STAGES], (t / C::V_STAGES) & 1, &aborted, kDecWaitNs) && ok;
+                    __syncwarp();
+                }
                 if (edge && !seen) {
                     // rows of V that are not every row's values: set aside, then 0
-                    uint8_t* v = smem + (t % STAGES) * C::STAGE + C::HALVES * C::HALF + tid * 128;
+                    uint8_t* v = smem + C::OFF_V + (t % C::V_STAGES) * C::STAGE + tid * 128;
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
