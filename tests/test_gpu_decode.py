@@ -372,3 +372,107 @@ def test_equals_the_prefill_with_every_block_kept(dtype):
     pr.check()
     a, b = p.out.double(), pr.out.double()
     assert float((a - b).norm() / b.norm()) <= (5e-2 if dtype == "fp8" else 5e-3) + 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,n,page,factors", [("bf16", 64, 8, 4, 64, False), ("fp8", 64, 8, 4, 64, True), ("fp8", 8, 1, 16, 16, False),
+                                                        ("bf16", 4, 1, 9, 256, False), ("fp8", 16, 2, 3, 128, True), ("bf16", 3, 3, 16, 0, False)])
+def test_drafts_over_long_keys(dtype, Hq, Hkv, n, page, factors):
+    """Several tokens over keys that many CTAs share: partial results of whole
+    tiles, tiles that end inside a page, new keys on both sides of a tile's edge."""
+    lk = [9000, 128 + n // 2, 256, 1023, n, 4097]
+    c = Case([n, n, n, 1, n, 2], lk, Hq, Hkv, 128, page, dtype, seed=20, factors=factors)
+    p = c.plan()
+    p.run()
+    c.check(p)
+    first = p.out.clone(), p.lse.clone()
+    p.workspace[256:].fill_(0xFF)
+    p.run()
+    p.check()
+    assert torch.equal(first[0], p.out) and torch.equal(first[1], p.lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(8, 2, 4), (8, 1, 16), (2, 2, 16), (4, 1, 2)])
+def test_drafts_at_head_dimension_64(Hq, Hkv, n):
+    c = Case([n, 1, n], [3000, 40, n + 7], Hq, Hkv, 64, 32, "bf16", seed=21)
+    p = c.plan()
+    p.run()
+    c.check(p)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("Hq,Hkv,n", [(8, 2, 1), (8, 1, 2), (16, 2, 5)])
+def test_rising_logits(dtype, Hq, Hkv, n):
+    """Logits that grow along the keys by far more than a weight may: the running
+    reference moves again and again, and the early keys' weights vanish."""
+    c = Case([n], [3000], Hq, Hkv, 128, 64, dtype, seed=22, spread=4.0)
+    flat = c.k.view(-1, Hkv, 128)
+    ramp = torch.linspace(0.02, 6.0, 3000, device="cuda")[:, None, None]
+    q = c.q.double().mean(0).sign().view(Hkv, Hq // Hkv, 128)[:, 0]  # keys along one row's signs
+    rows = (q[None] * ramp).float()
+    if dtype == "fp8":
+        raw = (rows / c.scales["k"][None, :, None]).clamp(-448, 448).to(E4M3)
+        flat.view(torch.uint8)[c.rows[0]] = raw.view(torch.uint8)
+    else:
+        flat[c.rows[0]] = rows.bfloat16()
+    p = c.plan()
+    p.run()
+    c.check(p)
+
+
+def test_many_drafting_sequences():
+    rs = np.random.RandomState(23)
+    lk = rs.randint(20, 400, 300).tolist()
+    lq = rs.randint(0, 6, 300).tolist()
+    lq[7] = 6
+    c = Case(lq, lk, 8, 1, 128, 16, "fp8", seed=23)
+    p = c.plan()
+    p.run()
+    c.check(p)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_drafts_in_a_captured_graph(dtype):
+    """Replays with other numbers of drafted tokens than at the capture."""
+    c = Case([4, 4, 4], [2000, 300, 700], 8, 1, 128, 64, dtype, seed=24)
+    p = c.plan()
+    p.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.run()
+    for lq in ([4, 4, 4], [1, 0, 3], [2, 4, 1]):
+        c.cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(lq)]), dtype=torch.int32))
+        p.out.zero_()
+        g.replay()
+        d = Case.__new__(Case)
+        d.__dict__.update(c.__dict__)
+        d.lq = lq
+        d.check(p)
+
+
+@pytest.mark.parametrize("scale_given", [False, True])
+def test_drafts_with_e4m3_output(scale_given):
+    c = Case([3, 4], [300, 2000], 8, 1, 128, 64, "fp8", seed=25)
+    sc = torch.linspace(0.002, 0.02, 8, device="cuda") if scale_given else None
+    p = c.plan(out_dtype=fp2.FP2_FP8_E4M3, out_scale=sc)
+    p.run()
+    c.check(p, out_scale=sc if scale_given else c.scales["v"].repeat_interleave(8))
+
+
+def test_drafts_with_a_bad_page_or_factor():
+    c = Case([4, 4], [900, 700], 8, 1, 128, 64, "fp8", seed=26, factors=True)
+    p = c.plan()
+    keep = int(c.table[0, 3])
+    c.table[0, 3] = 10 ** 6
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_DEVICE_BOUNDS, 3)
+    c.check(p, skip=(0,))
+    c.table[0, 3] = keep
+    c.fac["k"][1, 2, 0] = 0.0
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_INVALID_ARG, 5)
+    c.check(p, skip=(1,))
