@@ -192,7 +192,7 @@ cudaError_t join(cudaStream_t from, cudaStream_t to, cudaEvent_t e) {
 
 extern "C" {
 
-const char* fp2_version(void) { return "0.1.0"; }
+const char* fp2_version(void) { return "0.2.0"; }
 
 const char* fp2_status_string(fp2_status s) {
     switch (s) {

@@ -186,6 +186,31 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
             fetch_round(n0 + 32);
         };
         fetch_round(0);
+        // the queries and their scales, on their way together with the page ids (a
+        // row past the last repeats it: its results are not stored)
+        auto q_row = [&](int hx, int r) {
+            const int i = tile * R + min(r, rows - 1);
+            return static_cast<const uint8_t*>(D.q) +
+                   ((long long)(s.q0 + token_of(D, i)) * p.Hq + (group * D.hc + hx) * p.G + head_of(D, i)) * RB;
+        };
+        uint32_t q_raw[V::Q_SMEM ? 1 : NT][FP8 ? QC : 2 * QC];
+        float q_scale[NT][2], k_scale = 1.f;
+        if constexpr (!V::Q_SMEM) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint8_t* q = q_row(hs, nt * 8 + g) + 4 * t4;
+#pragma unroll
+                for (int i = 0; i < (FP8 ? QC : 2 * QC); ++i) q_raw[nt][i] = *reinterpret_cast<const uint32_t*>(q + 16 * i);
+            }
+        }
+        if constexpr (FP8) {
+            k_scale = p.k_scale[hk];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    q_scale[nt][e] = p.q_scale[hk * p.G + head_of(D, tile * R + min(nt * 8 + 2 * t4 + e, rows - 1))];
+        }
         begin_round(0);
         auto issue = [&](int i, int stage) {
             if (i >= steps) return;
@@ -211,34 +236,21 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
 
         // ---- this warp's query columns, running (m, l, o) ----
-        // operand registers of 16-value step c of row rq: two pairs of values
-        auto query = [&](int hx, int rq, int ch, int t, uint32_t& b0, uint32_t& b1) {
-            b0 = b1 = 0u;
-            if (rq >= rows) return;
-            const int tok = (tile * R + rq) / p.G, h = (group * D.hc + hx) * p.G + (tile * R + rq) % p.G;
-            const uint8_t* q = static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + tok) * p.Hq + h) * RB;
-            if constexpr (FP8) {
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(q + 16 * ch + 4 * t);
-                b0 = f16_of(x, false);
-                b1 = f16_of(x, true);
-            } else {
-                b0 = *reinterpret_cast<const uint32_t*>(q + 32 * ch + 4 * t);
-                b1 = *reinterpret_cast<const uint32_t*>(q + 32 * ch + 4 * t + 16);
-            }
-        };
         uint8_t* const q_smem = ring + kWarps * V::RING;
         if constexpr (V::Q_SMEM) {
             // [head][row][2 DH bytes], 16-byte chunk x at x ^ (row & 7) of each 8
             for (int y = threadIdx.x; y < D.hc * R * QC * 4; y += kThreads) {
                 const int t = y & 3, ch = y / 4 % QC, r = y / 4 / QC % R, hx = y / 4 / QC / R;
-                uint32_t b0, b1;
-                query(hx, r, ch, t, b0, b1);
+                const uint8_t* q = q_row(hx, r) + (FP8 ? 16 * ch : 32 * ch) + 4 * t;
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(q);
                 uint8_t* row = q_smem + hx * V::Q_BYTES + r * DH * 2;
-                *reinterpret_cast<uint32_t*>(row + (((2 * ch) ^ (r & 7)) << 4) + 4 * t) = b0;
-                *reinterpret_cast<uint32_t*>(row + (((2 * ch + 1) ^ (r & 7)) << 4) + 4 * t) = b1;
+                *reinterpret_cast<uint32_t*>(row + (((2 * ch) ^ (r & 7)) << 4) + 4 * t) = FP8 ? f16_of(x, false) : x;
+                *reinterpret_cast<uint32_t*>(row + (((2 * ch + 1) ^ (r & 7)) << 4) + 4 * t) =
+                    FP8 ? f16_of(x, true) : *reinterpret_cast<const uint32_t*>(q + 16);
             }
             __syncthreads();
         }
+        // operand registers of each 16-value step: two pairs of values
         uint32_t qf[V::Q_SMEM ? 1 : NT][QC][2];
         float sc[NT][2], neg_m[NT][2], l[NT][2], o[NT][MT][4];
         int last[NT][2];  // last visible key of rows 2 t4, 2 t4 + 1 of the tile
@@ -246,14 +258,16 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (!V::Q_SMEM) {
 #pragma unroll
-                for (int ch = 0; ch < QC; ++ch) query(hs, nt * 8 + g, ch, t4, qf[nt][ch][0], qf[nt][ch][1]);
+                for (int ch = 0; ch < QC; ++ch) {
+                    qf[nt][ch][0] = FP8 ? f16_of(q_raw[nt][ch], false) : q_raw[nt][2 * ch];
+                    qf[nt][ch][1] = FP8 ? f16_of(q_raw[nt][ch], true) : q_raw[nt][2 * ch + 1];
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = min(nt * 8 + 2 * t4 + e, rows - 1);
-                last[nt][e] = s.P + (tile * R + r) / p.G;
-                sc[nt][e] = D.qk_scale;
-                if constexpr (FP8) sc[nt][e] *= p.q_scale[hk * p.G + (tile * R + r) % p.G] * p.k_scale[hk];
+                last[nt][e] = s.P + token_of(D, tile * R + r);
+                sc[nt][e] = D.qk_scale * (FP8 ? q_scale[nt][e] * k_scale : 1.f);
                 neg_m[nt][e] = FLT_MAX;
                 l[nt][e] = 0.f;
             }
@@ -501,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 O = plus(O, *reinterpret_cast<const float4*>(ring + w * V::RING + (r * OS + col) * 4), f);
             }
             if (whole) {
-                const int tok = (tile * R + r) / p.G, hkv = group * D.hc + hx, h = hkv * p.G + (tile * R + r) % p.G;
+                const int tok = token_of(D, tile * R + r), hkv = group * D.hc + hx, h = hkv * p.G + head_of(D, tile * R + r);
                 put_out(D, s.q0 + tok, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
                 if (D.lse && col == 0) D.lse[(long long)(s.q0 + tok) * p.Hq + h] = lse_of(M, L);
             } else {
@@ -584,7 +598,7 @@ __device__ __forceinline__ void add_parts(const DecodeParams& D, const Item& ite
 template <bool FP8, int R>
 __device__ __forceinline__ void finish_row(const DecodeParams& D, const Item& item, int hx, int r, int col, float4 O, float M, float L) {
     const KParams& p = D.p;
-    const int hkv = item.a.z * D.hc + hx, t = (item.a.w * R + r) / p.G, h = hkv * p.G + (item.a.w * R + r) % p.G;
+    const int hkv = item.a.z * D.hc + hx, t = token_of(D, item.a.w * R + r), h = hkv * p.G + head_of(D, item.a.w * R + r);
     put_out(D, item.a.y + t, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
     if (D.lse && col == 0) D.lse[(long long)(item.a.y + t) * p.Hq + h] = lse_of(M, L);
 }
@@ -653,7 +667,8 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using V = Variant<DH, FP8, NT>;
     // more than 8 packed rows at head dimension 128: whole tiles on the tensor core
     constexpr bool TILES = DH == 128 && NT == 4;
-    const int packed = D.p.max_seqlen_q * D.p.G;
+    // (at least one: lengths above a limit of 0 have to be recorded)
+    const int packed = D.p.max_seqlen_q > 0 ? D.p.max_seqlen_q * D.p.G : 1;
     D.hc = D.p.Hkv % (TILES ? 2 : V::HEADS) ? 1 : TILES ? 2 : V::HEADS;
     D.groups = D.p.Hkv / D.hc;
     D.tiles_max = (packed + V::R - 1) / V::R;

@@ -31,7 +31,7 @@ template <int R, int UNIT>
 __device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const SeqInfo& s) {
     Shape x;
     x.per_item = (s.Lk + UNIT - 1) / UNIT;
-    x.tiles = (s.Lq * D.p.G + R - 1) / R;
+    x.tiles = ((s.Lq << D.g_shift) + R - 1) / R;
     x.units = (long long)x.per_item * x.tiles * D.groups;
     return x;
 }
@@ -41,6 +41,9 @@ __device__ __forceinline__ long long seq_units(const DecodeParams& D, int b, Seq
     if (!load_seq(D.p, b, s) || s.Lq == 0) return 0;
     return seq_shape<R, UNIT>(D, s).units;
 }
+// Packed row i of a sequence and KV head: its token, its query head within the group.
+__device__ __forceinline__ int token_of(const DecodeParams& D, int i) { return i >> D.g_shift; }
+__device__ __forceinline__ int head_of(const DecodeParams& D, int i) { return i & (D.p.G - 1); }
 // a / b of values that mostly fit 32 bits.
 __device__ __forceinline__ long long quotient(long long a, long long b) {
     if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
@@ -178,14 +181,13 @@ __device__ __forceinline__ bool next_segment(const DecodeParams& D, Share& x, Se
     const int item = (int)quotient(x.u - x.seq_at, sh.per_item);
     g.item_at = x.seq_at + (long long)item * sh.per_item;
     g.per_item = sh.per_item;
-    g.group = item / sh.tiles;
-    g.tile = item % sh.tiles;
+    g.group = sh.tiles == 1 ? item : item / sh.tiles;
+    g.tile = item - g.group * sh.tiles;
     g.x0 = (int)(x.u - g.item_at);
     g.x1 = (int)min((long long)sh.per_item, x.u_end - g.item_at);
-    // packed row r is token (tile * R + r) / G, head r % G of the group
-    g.rows = min(R, x.s.Lq * p.G - g.tile * R);
-    g.t_first = g.tile * R / p.G;
-    g.t_last = (g.tile * R + g.rows - 1) / p.G;
+    g.rows = min(R, (x.s.Lq << D.g_shift) - g.tile * R);
+    g.t_first = token_of(D, g.tile * R);
+    g.t_last = token_of(D, g.tile * R + g.rows - 1);
     g.seen_all = x.s.P + g.t_first + 1;
     g.seen_any = x.s.P + g.t_last + 1;
     return true;
@@ -204,7 +206,7 @@ __device__ __forceinline__ void put_out(const DecodeParams& D, long long row, in
     const KParams& p = D.p;
     const long long at = (row * p.Hq + h) * p.d + col;
     if (p.out_fp8) {
-        const float sc = p.out_scale ? p.out_scale[h] : p.v_scale[h / p.G];
+        const float sc = p.out_scale ? p.out_scale[h] : p.v_scale[h >> D.g_shift];
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D.out) + at) = pack_e4m3x4(x.x / sc, x.y / sc, x.z / sc, x.w / sc);
     } else {
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(D.out) + at) =

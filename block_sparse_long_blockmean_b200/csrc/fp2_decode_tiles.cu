@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
         while (!dead && next_segment<R, kTileKeys>(D, x, g)) {
             const SeqInfo& s = x.s;
             const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
-            auto token = [&](int r) { return (g.tile * R + r) / p.G; };
-            auto head = [&](int r) { return hk * p.G + (g.tile * R + r) % p.G; };
+            auto token = [&](int r) { return token_of(D, g.tile * R + r); };
+            auto head = [&](int r) { return hk * p.G + head_of(D, g.tile * R + r); };
             auto q_row = [&](int r) {
                 return static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * RB;
             };

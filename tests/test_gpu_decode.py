@@ -476,3 +476,18 @@ def test_drafts_with_a_bad_page_or_factor():
         p.check()
     assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_INVALID_ARG, 5)
     c.check(p, skip=(1,))
+
+
+def test_a_step_in_which_every_sequence_rests():
+    c = Case([0, 0], [100, 40], seed=27, pad=1)
+    p = c.plan(max_seqlen_q=0)
+    p.out.fill_(3.0)
+    p.run()
+    p.check()
+    assert (p.out == 3).all()
+    c.cu.copy_(torch.tensor([0, 0, 1], dtype=torch.int32))  # a token above the limit of 0
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_INVALID_ARG, 1)
+    assert (p.out == 3).all()
