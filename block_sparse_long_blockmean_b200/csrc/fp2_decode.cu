@@ -47,11 +47,8 @@ struct Variant {
     static constexpr int STAGES = RB == 256 ? 3 : NT == 4 ? 5 : 4;
     static constexpr int RING = STAGES * STAGE;             // of one warp
     static constexpr bool Q_SMEM = NT == 4;                 // queries: shared memory or registers
-    static constexpr int Q_BYTES = Q_SMEM ? R * DH * 2 : 0; // of one head, as 16-bit values
-    // two adjacent KV heads an item where two CTAs still fit an SM: a token's rows
-    // of both are one piece of 256 or 512 bytes for the DRAM
-    static constexpr int HEADS = RB == 256 && Q_SMEM ? 1 : kDecHeads;
-    static constexpr int SMEM = kWarps * RING + HEADS * Q_BYTES;
+    static constexpr int Q_BYTES = Q_SMEM ? R * DH * 2 : 0; // of one head
+    static constexpr int SMEM = kWarps * RING + kDecHeads * Q_BYTES;
     static constexpr int PER_SM = RB == 256 || NT > 1 ? 2 : 3;  // CTAs (shared memory and registers)
     static constexpr int CTAS = 148 * PER_SM;
     static constexpr int OS = DH + 4;                       // row stride of the warps' join
@@ -238,15 +235,12 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         // ---- this warp's query columns, running (m, l, o) ----
         uint8_t* const q_smem = ring + kWarps * V::RING;
         if constexpr (V::Q_SMEM) {
-            // [head][row][2 DH bytes], 16-byte chunk x at x ^ (row & 7) of each 8
-            for (int y = threadIdx.x; y < D.hc * R * QC * 4; y += kThreads) {
-                const int t = y & 3, ch = y / 4 % QC, r = y / 4 / QC % R, hx = y / 4 / QC / R;
-                const uint8_t* q = q_row(hx, r) + (FP8 ? 16 * ch : 32 * ch) + 4 * t;
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(q);
-                uint8_t* row = q_smem + hx * V::Q_BYTES + r * DH * 2;
-                *reinterpret_cast<uint32_t*>(row + (((2 * ch) ^ (r & 7)) << 4) + 4 * t) = FP8 ? f16_of(x, false) : x;
-                *reinterpret_cast<uint32_t*>(row + (((2 * ch + 1) ^ (r & 7)) << 4) + 4 * t) =
-                    FP8 ? f16_of(x, true) : *reinterpret_cast<const uint32_t*>(q + 16);
+            // [head][row][RB bytes], 16-byte chunk x at x ^ (row & 7) of each 8
+            static_assert(!FP8, "16-bit queries");
+            for (int y = threadIdx.x; y < D.hc * R * (RB / 16); y += kThreads) {
+                const int ch = y % (RB / 16), r = y / (RB / 16) % R, hx = y / (RB / 16) / R;
+                *reinterpret_cast<uint4*>(q_smem + hx * V::Q_BYTES + r * RB + ((ch ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<const uint4*>(q_row(hx, r) + ch * 16);
             }
             __syncthreads();
         }
@@ -268,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 const int r = min(nt * 8 + 2 * t4 + e, rows - 1);
                 last[nt][e] = s.P + token_of(D, tile * R + r);
                 sc[nt][e] = D.qk_scale * (FP8 ? q_scale[nt][e] * k_scale : 1.f);
+                // (a scale of 0 stands for a head of zeros; a masked logit stays -inf)
+                if (FP8 && sc[nt][e] == 0.f) sc[nt][e] = 1e-30f;
                 neg_m[nt][e] = FLT_MAX;
                 l[nt][e] = 0.f;
             }
@@ -669,7 +665,7 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     constexpr bool TILES = DH == 128 && NT == 4;
     // (at least one: lengths above a limit of 0 have to be recorded)
     const int packed = D.p.max_seqlen_q > 0 ? D.p.max_seqlen_q * D.p.G : 1;
-    D.hc = D.p.Hkv % (TILES ? 2 : V::HEADS) ? 1 : TILES ? 2 : V::HEADS;
+    D.hc = D.p.Hkv % kDecHeads ? 1 : kDecHeads;
     D.groups = D.p.Hkv / D.hc;
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;

@@ -50,13 +50,12 @@ struct Tile {
     static constexpr int WARPS = 4 * WGS + 2, THREADS = 32 * WARPS;
     // K is free once its logits are there, V only after its product
     static constexpr int K_STAGES = FP8 ? 2 : 3, V_STAGES = 3;
-    static constexpr int P_BUFS = 1;                      // weights' tiles
     static constexpr int TERMS = FP8 ? 4 : 2;             // operand terms of a weight
     static constexpr int PV_N = TERMS * kTileRows;        // columns of the second product: 128 bytes a key
     static constexpr int KSTEP = FP8 ? 32 : 16;           // k of one product
     static constexpr int OFF_V = K_STAGES * STAGE;
     static constexpr int OFF_P = OFF_V + V_STAGES * STAGE;
-    static constexpr int OFF_Q = OFF_P + P_BUFS * HALF;
+    static constexpr int OFF_Q = OFF_P + HALF;
     static constexpr int SMEM = OFF_Q + HALVES * kTileRows * 128;
     static constexpr int O_COL = 64;                      // TMEM: S twice, then O
     static constexpr uint32_t TMEM = FP8 ? 256 : 128;
@@ -272,10 +271,9 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t at = dv + (uint32_t)(v_stage * (C::STAGE >> 4));
-                        const uint64_t bt = dp + (uint32_t)(i % C::P_BUFS * (C::HALF >> 4));
 #pragma unroll
                         for (int ks = 0; ks < kTileKeys / C::KSTEP; ++ks) {  // KSTEP keys each
-                            const uint64_t ad = at + (uint32_t)(ks * C::KSTEP * 8), bd = bt + (uint32_t)(ks * C::KSTEP * 8);
+                            const uint64_t ad = at + (uint32_t)(ks * C::KSTEP * 8), bd = dp + (uint32_t)(ks * C::KSTEP * 8);
                             const uint32_t acc = n > 1 || ks > 0;
                             if constexpr (FP8) mma_f8_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
                             else mma_bf16_ss(tmem + C::O_COL, ad, bd, idesc_pv, acc);
@@ -493,11 +491,11 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                         chunk[2 * h + 1] = 4 + first / 8 + h;
                     }
                 }
-                if (n >= C::P_BUFS) {  // the buffer's last reader
-                    ok = product_done(t - C::P_BUFS) && ok;
+                if (n >= 1) {  // the weights' last reader
+                    ok = product_done(t - 1) && ok;
                     __syncwarp();
                 }
-                uint8_t* const p_row = smem + C::OFF_P + t % C::P_BUFS * C::HALF + tid * 128;
+                uint8_t* const p_row = smem + C::OFF_P + tid * 128;
 #pragma unroll
                 for (int k = 0; k < 4 * H / 16; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
                 if (edge) {

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const __grid_cons
     // a thread takes `per` consecutive sequences
     const int per = (S + kMapThreads - 1) / kMapThreads;
     const int b0 = min(S, (int)threadIdx.x * per), b1 = min(S, b0 + per);
-    auto pages = [&](int n) { return (n + p.page_size - 1) >> p.page_shift; };
+    auto pages = [&](int n) { return (n >> p.page_shift) + ((n & (p.page_size - 1)) != 0); };
     auto read = [&](int b, int& pre, int& n) {
         pre = p.prefix[b];
         n = p.fresh[b];
@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const __grid_cons
         int b = i0 < live ? owner(cu, S, (int)i0) : S - 1;
 #pragma unroll
         for (int e = 0; e < TOKENS; ++e) {
-            const int i = (int)i0 + e;
             pos[e] = 0;
             id[e] = -1;
-            if (i < live) {
+            if (i0 + e < live) {
+                const int i = (int)i0 + e;
                 while (i >= cu[b + 1]) ++b;
                 pos[e] = had[b] + (i - cu[b]);
                 const int k = pos[e] >> p.page_shift, old = pages(had[b]);
@@ -189,7 +189,7 @@ static cudaError_t launch(const MapParams& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     const int per_cta = TOKENS * kMapThreads;
-    int ctas = (p.total_q + per_cta - 1) / per_cta;
+    int ctas = (int)(((long long)p.total_q + per_cta - 1) / per_cta);
     ctas = ctas < 1 ? 1 : ctas > 296 ? 296 : ctas;
     return launch_early(page_map_kernel<TOKENS>, dim3(ctas), kMapThreads, smem, s, p);
 }

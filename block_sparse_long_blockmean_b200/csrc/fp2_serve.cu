@@ -242,6 +242,17 @@ fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
         return FP2_ERR_INVALID_ARG;
     if (P->total_q == 0) return FP2_OK;
     if (!page_table && P->total_k == 0) return FP2_ERR_INVALID_ARG;
+    // shares read queries, keys and values while others already write their rows
+    const size_t nq = (size_t)P->total_q * P->num_q_heads * P->head_dim,
+                 rows = page_table ? (size_t)P->num_pages * P->page_size : (size_t)P->total_k,
+                 nc = rows * P->num_kv_heads * P->head_dim * (fp8 ? 1 : 2);
+    const struct { const void* p; size_t n; } in[] = {{q, nq * (fp8 ? 1 : 2)}, {k_cache, nc}, {v_cache, nc}},
+        outs[] = {{out, nq * (P->out_dtype == FP2_FP8_E4M3 ? 1 : 2)},
+                  {lse, lse ? (size_t)P->total_q * P->num_q_heads * sizeof(float) : 0}};
+    for (const auto& o : outs)
+        for (const auto& i : in)
+            if (o.n && overlap(o.p, o.n, i.p, i.n)) return FP2_ERR_INVALID_ARG;
+    if (outs[1].n && overlap(lse, outs[1].n, out, outs[0].n)) return FP2_ERR_INVALID_ARG;
 
     uint8_t* ws = static_cast<uint8_t*>(P->workspace);
     fp2::DecodeParams D;
@@ -260,8 +271,9 @@ fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
     kp.max_pages = page_table ? P->max_pages_per_seq : 0;
     kp.num_pages = page_table ? P->num_pages : 0;
     kp.max_seqlen_q = P->max_seqlen_q;
-    kp.max_seqlen_k = P->max_seqlen_k;
-    kp.nkb_max = (P->max_seqlen_k + block - 1) / block;
+    // (lengths are rounded up to whole tiles in 32 bits)
+    kp.max_seqlen_k = P->max_seqlen_k <= INT32_MAX - 256 ? P->max_seqlen_k : INT32_MAX - 256;
+    kp.nkb_max = (int)(((long long)P->max_seqlen_k + block - 1) / block);
     kp.fp8 = fp8;
     kp.uses_kv = 1;
     kp.out_fp8 = P->out_dtype == FP2_FP8_E4M3;

@@ -473,6 +473,7 @@ class _Step:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
             fresh = True
         else:
+            _need(workspace, "workspace", (torch.uint8,), self.device)
             fresh = False
         self.workspace = workspace
         self.params.workspace = workspace.data_ptr()

@@ -372,7 +372,8 @@ typedef struct fp2_append_io {
  * in fp32, rounded once: to bf16, or (FP2_FP8_E4M3) to e4m3 of x / scale with
  * params->q_scale, k_scale, v_scale, saturating.  v is only stored.  A slot
  * outside the cache other than a negative one records FP2_ERR_DEVICE_BOUNDS
- * (detail 7) and is not written; of two tokens with one slot either may win.
+ * (detail 7) and is not written.  Slots other than -1 have to differ: of two
+ * tokens with one slot, the row ends up with parts of either.
  * q_out may be q itself when q is bf16 rows without a gap; the other buffers
  * must not overlap.  q, k and v are 8-byte aligned, weights and outputs 16.
  * Caches quantised per key block (params->k_block_factor) are not written by
@@ -396,7 +397,8 @@ size_t fp2_decode_workspace_size(const fp2_params* params);
  * kernel.  Arguments, supported shapes and dtypes as fp2_attn (block matters
  * for k_block_factor and the page size only); out as fp2_prefill's, rows behind
  * the last sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys
- * may hold anything, NaN included.  group_masks, attn_kernel and the debug
+ * may hold anything, NaN included.  out and lse must not overlap the inputs or
+ * each other.  group_masks, attn_kernel and the debug
  * fields have no effect.  The workspace's contents need not survive between
  * calls; calls that share one must be ordered on a stream.
  * max_seqlen_q above FP2_DECODE_MAX_Q: FP2_ERR_UNSUPPORTED (fp2_prefill takes

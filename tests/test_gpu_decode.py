@@ -98,9 +98,10 @@ class Case:
             a = int(self.cu[b])
             got, got_lse = plan.out[a:a + self.lq[b]].double(), plan.lse[a:a + self.lq[b]].double()
             assert torch.isfinite(got).all() and torch.isfinite(got_lse).all(), b
-            off, off_lse = (got - ref).abs() / tol, (got_lse - lse).abs() / tol_lse
-            assert off.max() <= 1, (b, float(off.max()), float((got - ref).abs().max()))
-            assert off_lse.max() <= 1, (b, float(off_lse.max()))
+            # (a bound of 0, where every value is 0, asks for the value itself)
+            off, off_lse = (got - ref).abs(), (got_lse - lse).abs()
+            assert (off <= tol).all(), (b, float((off / tol).nan_to_num(0).max()), float(off.max()))
+            assert (off_lse <= tol_lse).all(), (b, float((off_lse / tol_lse).max()))
 
 
 SHAPES = [(4, 1, 64), (2, 2, 64), (16, 2, 64), (8, 2, 128), (4, 4, 128), (4, 2, 128), (8, 1, 128)]
@@ -486,6 +487,52 @@ def test_a_step_in_which_every_sequence_rests():
     p.check()
     assert (p.out == 3).all()
     c.cu.copy_(torch.tensor([0, 0, 1], dtype=torch.int32))  # a token above the limit of 0
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_INVALID_ARG, 1)
+    assert (p.out == 3).all()
+
+
+@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_a_scale_of_zero_is_a_head_of_zeros(n, which):
+    c = Case([n, n], [170, 40], 8, 1, 128, 16, "fp8", seed=28)
+    c.scales[which][0] = 0.0
+    p = c.plan()
+    p.run()
+    c.check(p)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_no_limit_on_the_keys(n):
+    """max_seqlen_k as large as its type: a bound only, nothing is sized by it."""
+    c = Case([n, n], [300, 40], 8, 1, 128, 64, seed=29)
+    p = c.plan(max_seqlen_k=2 ** 31 - 1)
+    p.run()
+    c.check(p)
+    c.seqlens_k[0] = 2 ** 31 - 1  # more than its pages hold
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert e.value.detail == 1
+    c.check(p, skip=(0,))
+
+
+def test_offsets_that_wrap_are_refused():
+    """Row and key offsets whose sums pass 32 bits are bad lengths, not small ones."""
+    c = Case([1, 1], [300, 40], 8, 1, 128, 0, seed=30)
+    p = c.plan()
+    cu_k = c.cu_k.clone()
+    c.cu_k[0] = 2 ** 31 - 100
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_DEVICE_BOUNDS, 1)
+    c.check(p, skip=(0,))
+    c.cu_k.copy_(cu_k)
+    c.cu.copy_(torch.tensor([2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1], dtype=torch.int32))
+    p.out.fill_(3.0)
     p.run()
     with pytest.raises(fp2.Fp2Error) as e:
         p.check()

@@ -73,6 +73,21 @@ def test_long_prompts():
     compare(m, R.page_map(prefix, new, table, free, used, 64, sum(new)))
 
 
+def test_no_limit_on_the_keys():
+    prefix, new = [10, 40, 0], [7, 30, 20]
+    m, table, free, used = setup(prefix, new, 16)
+    m.params.max_seqlen_k = 2 ** 31 - 1
+    m.run()
+    m.check()
+    compare(m, R.page_map(prefix, new, table, free, used, 16, sum(new)))
+    m.prefix_lens[1] = 2 ** 31 - 31  # more than a row of the table holds
+    m.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        m.check()
+    assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_DEVICE_BOUNDS, 1)
+    assert m.cu_seqlens.tolist() == [0] * 4
+
+
 @pytest.mark.parametrize("what,status,detail", [
     ("new_negative", fp2.FP2_ERR_INVALID_ARG, 1), ("new_large", fp2.FP2_ERR_INVALID_ARG, 1),
     ("prefix_negative", fp2.FP2_ERR_INVALID_ARG, 1), ("keys_large", fp2.FP2_ERR_INVALID_ARG, 1),

@@ -171,6 +171,18 @@ def test_decode_refuses_pointers_types_and_blocks(lib):
     assert call_decode(lib, params(total_k=0), table=None) == INVALID
 
 
+def test_decode_refuses_outputs_over_inputs(lib):
+    P = params()
+    q, k, v, out = (n << 32 for n in (1, 2, 3, 4))
+    nq = P.total_q * P.num_q_heads * P.head_dim * 2
+    nc = P.num_pages * P.page_size * P.num_kv_heads * P.head_dim * 2
+    for at in (q, q + nq - 16, q - nq + 16, k, k + nc - 16, v, v - nq + 16):
+        assert call_decode(lib, P, out=at) == INVALID
+    nl = P.total_q * P.num_q_heads * 4
+    for at in (q, q + nq - 4, q - nl + 4, k + 64, v + nc - 4, out, out + nq - 4, out - nl + 4):
+        assert call_decode(lib, P, lse=at) == INVALID
+
+
 # --------------------------------------------------- the Python handles' ----
 
 def test_handles_refuse_what_the_abi_cannot_see():
@@ -197,3 +209,15 @@ def test_handles_refuse_what_the_abi_cannot_see():
         fp2.make_decode(h(4, 8, 128), h(64, 2, 128), h(64, 2, 128).float(), i(5), **dec)
     with pytest.raises(ValueError):
         fp2.make_decode(h(4, 8, 128), h(4, 16, 2, 128), h(4, 16, 2, 128), i(5), page_table=i(4, 3), page_size=32, **dec)
+
+
+def test_handles_refuse_other_workspaces():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    kw = dict(page_size=16, num_pages=10, total_q=4, max_seqlen_q=4, max_seqlen_k=40)
+    args = (i(3), i(3), i(3, 4), i(9), i(1))
+    with pytest.raises(TypeError):
+        fp2.make_page_map(*args, workspace=torch.zeros(256), **kw)
+    with pytest.raises(ValueError):
+        fp2.make_page_map(*args, workspace=torch.zeros(1, dtype=torch.uint8).expand(256), **kw)
+    with pytest.raises(ValueError):
+        fp2.make_page_map(*args, workspace=torch.zeros(256, dtype=torch.uint8, device="meta"), **kw)
