@@ -11,6 +11,15 @@
 // A head of a token is held by D / 8 lanes with 8 values each, as two groups
 // of 4, values a..a+3 and b..b+3 with b = a + rot/2, so that a half-split pair
 // (i, i + rot/2) and an adjacent pair (2i, 2i + 1) both stay inside a lane.
+//
+// Bound by the rows' bytes.  A lane copies its own 8-byte groups a step ahead into
+// shared memory: no lane waits for another's, 8-byte rows of any stride will do, and
+// no register holds a row on its way.  32768 tokens of 64 + 2 x 8 heads of 128, bf16 to
+// e4m3 (1007 MB): 155 us, 6.48 TB/s; the rows in registers, loaded as they were
+// needed: 178 us; a step ahead in registers: 242 us.  Steps of 4 groups, two of them
+// in shared memory, 6 CTAs on an SM: 155 us; 3 steps of 4: 159; 4 of 4: 196 (the
+// rest of the L1 cache is too small); 4 of 2: 164; 2 of 3: 164; 2 of 6: 165.
+// Small calls are bound by their launch (64 tokens: 2.4 us).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -23,7 +32,8 @@ namespace fp2 {
 namespace {
 
 constexpr int kAppThreads = 128, kAppWarps = kAppThreads / 32;
-constexpr int kAppDepth = 4;  // groups of heads whose rows a warp loads at once
+constexpr int kAppDepth = 4;   // groups of heads of a step
+constexpr int kAppStages = 2;  // steps in shared memory or on their way there
 
 struct Quad {
     float2 x, y;
@@ -43,6 +53,14 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 swapped(float2 a) { return make_float2(a.y, a.x); }
 
+// 8 bytes to shared memory, for this thread alone to read after wait_copies().
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the N latest groups of copies
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // The one rounding: to bf16, or to e4m3 (the caller has divided by the scale).
 template <bool FP8>
 __device__ __forceinline__ void store4(uint8_t* to, Quad v) {
@@ -56,7 +74,7 @@ __device__ __forceinline__ void store4(uint8_t* to, Quad v) {
 // grid (ceil(T / warps), chunks): a warp takes one token and a chunk of its
 // groups of 32 / (D / 8) heads (q's, then k's, then v's).
 template <int D, bool FP8, bool ADJACENT>
-__global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 6) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int HL = D / 8, HPW = 32 / HL;
     const int lane = threadIdx.x & 31, l = lane % HL;
     const int tok = blockIdx.x * kAppWarps + (threadIdx.x >> 5);
@@ -64,13 +82,42 @@ __global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_con
     if (tok >= p.total_q) return;
     const int rot = p.rot;
     const bool rotates = l < rot / 8;
+    int slot = p.slots[tok];
+    const double pos = rotates ? (double)p.positions[tok] : 0.;
     // this lane's two groups of four values
     const int ia = rotates ? 4 * l : rot + 4 * (l - rot / 8);
     const int ib = rotates ? rot / 2 + 4 * l : ia + (D - rot) / 2;
-    int slot = p.slots[tok];
+    // steps of kAppDepth groups: q's, then k's, then v's
+    const int nq = (p.Hq + HPW - 1) / HPW, nk = (p.Hkv + HPW - 1) / HPW;
+    const int g0 = blockIdx.y * p.chunk, g1 = min(g0 + p.chunk, nq + 2 * nk);
+    const int k_from = max(g0, nq) - nq, v_from = max(g0, nq + nk) - nq - nk;
+    const int q_to = min(g1, nq), k_to = min(g1, nq + nk) - nq, v_to = g1 - nq - nk;
+    auto steps_of = [](int from, int to) { return to > from ? (to - from + kAppDepth - 1) / kAppDepth : 0; };
+    const int q_steps = steps_of(g0, q_to), qk_steps = q_steps + steps_of(k_from, k_to), steps = qk_steps + steps_of(v_from, v_to);
+    // a lane's own 16 bytes of each group, so that no lane waits for another's
+    __shared__ __align__(16) uint4 rows[kAppStages][kAppDepth][kAppThreads];
+    auto fetch = [&](int n) {
+        if (n < steps) {
+            const bool is_q = n < q_steps, is_k = !is_q && n < qk_steps;
+            const int g = is_q ? g0 + n * kAppDepth : is_k ? k_from + (n - q_steps) * kAppDepth : v_from + (n - qk_steps) * kAppDepth;
+            const int to = is_q ? q_to : is_k ? k_to : v_to, heads = is_q ? p.Hq : p.Hkv;
+            const uint16_t* src = static_cast<const uint16_t*>(is_q ? p.q : is_k ? p.k : p.v) +
+                                  (long long)tok * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) + (g * HPW + lane / HL) * D;
+            const uint32_t dst = smem_u32(&rows[n % kAppStages][0][threadIdx.x]);
+#pragma unroll
+            for (int i = 0; i < kAppDepth; ++i)
+                if (g + i < to && (g + i) * HPW + lane / HL < heads) {
+                    copy8(dst + i * (kAppThreads * 16), src + i * HPW * D + ia);
+                    copy8(dst + i * (kAppThreads * 16) + 8, src + i * HPW * D + ib);
+                }
+        }
+        end_copies();
+    };
+#pragma unroll
+    for (int n = 0; n < kAppStages - 1; ++n) fetch(n);
+    int now = 0;
     Quad ca = {{1.f, 1.f}, {1.f, 1.f}}, cb = ca, sa = {{0.f, 0.f}, {0.f, 0.f}}, sb = sa;  // cos, -+ sin
     if (rotates) {
-        const double pos = (double)p.positions[tok];
         float c[4], s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -100,14 +147,11 @@ __global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_con
         slot = -1;
     }
 
-    const int nq = (p.Hq + HPW - 1) / HPW, nk = (p.Hkv + HPW - 1) / HPW;
-    const int g0 = blockIdx.y * p.chunk, g1 = min(g0 + p.chunk, nq + 2 * nk);
     // groups [from, to) of one kind; TURN: norm and rotation, else as they are
-    auto stream = [&](auto turn, int from, int to, const void* src, long long stride, void* dst, long long row, int heads,
+    auto stream = [&](auto turn, int from, int to, void* dst, long long row, int heads,
                       const float* weight, const float* scale) {
         constexpr bool TURN = decltype(turn)::value;
         if (from >= to) return;
-        const uint16_t* in = static_cast<const uint16_t*>(src) + (long long)tok * stride;
         const long long out = row * heads * D;
         Quad wca = ca, wcb = cb, wsa = sa, wsb = sb;
         if (TURN && weight) {
@@ -124,32 +168,29 @@ __global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_con
             }
         }
         const bool norm = TURN && weight;
-        // this lane's first values of the present step; a group is GS values on
+        // where this lane's values of the present step go; a group is GS values on
         constexpr int GS = HPW * D, ES = FP8 ? 1 : 2;
-        const uint16_t* ra = in + (from * HPW + lane / HL) * D + ia;
-        const uint16_t* rb = ra + (ib - ia);
         uint8_t* wa = static_cast<uint8_t*>(dst) + (out + (from * HPW + lane / HL) * D + ia) * ES;
         uint8_t* wb = wa + (ib - ia) * ES;
         [[maybe_unused]] const float* sp = FP8 ? scale + from * HPW + lane / HL : nullptr;
         auto step = [&](auto full, int g) {
             constexpr bool FULL = decltype(full)::value;  // kAppDepth whole groups
-            uint2 raw[kAppDepth][2];
             float inv[kAppDepth];
+            fetch(now + kAppStages - 1);
             auto on = [&](int i) { return FULL || (g + i < to && (g + i) * HPW + lane / HL < heads); };
 #pragma unroll
             for (int i = 0; i < kAppDepth; ++i) {
-                raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
                 inv[i] = 1.f;
-                if (on(i)) {
-                    raw[i][0] = *reinterpret_cast<const uint2*>(ra + i * GS);
-                    raw[i][1] = *reinterpret_cast<const uint2*>(rb + i * GS);
-                    if constexpr (FP8) inv[i] = sp[i * HPW];
-                }
+                if (FP8 && on(i)) inv[i] = sp[i * HPW];
             }
+            wait_copies<kAppStages - 1>();
+            const uint4* mine = &rows[now % kAppStages][0][threadIdx.x];
 #pragma unroll
             for (int i = 0; i < kAppDepth; ++i) {
                 if (!FULL && g + i >= to) break;
-                Quad a = unpack(raw[i][0]), b = unpack(raw[i][1]);
+                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                if (on(i)) raw = mine[i * kAppThreads];
+                Quad a = unpack(make_uint2(raw.x, raw.y)), b = unpack(make_uint2(raw.z, raw.w));
                 // (the reciprocal is off by 2^-23 of its value, far below e4m3's 2^-4)
                 float r = FP8 ? __fdividef(1.f, inv[i]) : 1.f;
                 if constexpr (TURN) {
@@ -184,8 +225,7 @@ __global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_con
                     store4<FP8>(wb + i * GS * ES, b);
                 }
             }
-            ra += kAppDepth * GS;
-            rb += kAppDepth * GS;
+            ++now;
             wa += kAppDepth * GS * ES;
             wb += kAppDepth * GS * ES;
             if constexpr (FP8) sp += kAppDepth * HPW;
@@ -195,9 +235,9 @@ __global__ void __launch_bounds__(kAppThreads, 7) append_kernel(const __grid_con
             for (; g + kAppDepth <= to; g += kAppDepth) step(std::true_type{}, g);
         for (; g < to; g += kAppDepth) step(std::false_type{}, g);
     };
-    stream(std::true_type{}, g0, min(g1, nq), p.q, p.q_stride, p.q_out, tok, p.Hq, p.q_weight, p.q_scale);
-    stream(std::true_type{}, max(g0, nq) - nq, min(g1, nq + nk) - nq, p.k, p.k_stride, p.k_cache, slot, p.Hkv, p.k_weight, p.k_scale);
-    stream(std::false_type{}, max(g0, nq + nk) - nq - nk, g1 - nq - nk, p.v, p.v_stride, p.v_cache, slot, p.Hkv, nullptr, p.v_scale);
+    stream(std::true_type{}, g0, q_to, p.q_out, tok, p.Hq, p.q_weight, p.q_scale);
+    stream(std::true_type{}, k_from, k_to, p.k_cache, slot, p.Hkv, p.k_weight, p.k_scale);
+    stream(std::false_type{}, v_from, v_to, p.v_cache, slot, p.Hkv, nullptr, p.v_scale);
 }
 
 template <int D, bool FP8>
