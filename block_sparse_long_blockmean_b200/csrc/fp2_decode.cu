@@ -18,10 +18,15 @@
 // the 16 rows of an m16n8 product and 8 packed query rows as its columns:
 //   S^T (16 keys x 8 rows)  = K (16 x d) Q^T (d x 8)
 //   O^T (d x 8 rows)       += V^T (d x 16 keys) P^T (16 keys x 8 rows)
-// so that a tile of one token and at most 8 group heads wastes nothing, and a
-// lane holds the same two rows of S^T and O^T: the softmax's scaling never
-// crosses lanes.  Decoding reads each K and V byte once for at most 4 tiles of
-// 8 rows; it is bound by the cache's bytes, not by these products.
+// so that a tile of one token and 8 group heads wastes nothing, and a lane holds the
+// same two rows of S^T and O^T: the softmax's scaling never crosses lanes.
+//
+// Bound by the cache's bytes, each read once.  One sequence of 131072 bf16 keys, 32
+// heads over 8 (537 MB): 89 us, 6.0 TB/s; 128 ragged ones to 8191 keys (2.13 GB): 334
+// us, 6.4 TB/s; 8 e4m3 ones of 4K to 64K (486 MB): 89 us, 5.5 TB/s; 8 ragged bf16
+// ones to 4097 (73 MB): 24 us, of which 4 pass before the first keys are there and 5
+// in the join; one of 1024: 7.3 us, the two launches.  Loads alone reach 6.55 TB/s in
+// pieces of 256 bytes and 5.7 in pieces of 128.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,8 +38,13 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = kDecBox;  // keys of a unit: one copy
+constexpr int kHeadBytes = 1024;  // of the heads' rows of a token that are read together
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
+// Four warps a CTA, each with a ring of its own: a CTA of 8 warps on each SM leaves it
+// idle at a segment's end (512 sequences of 500 e4m3 keys: 231 us, two of 4 warps 177).
+// One tiled copy a unit, head and 128 bytes; a bulk copy per row took 134 us where
+// this takes 95 (128-byte rows: the copies' number counts).
 // A stage of a warp's ring holds the K and V rows of one unit and head, each as
 // RB / 128 tiles of 16 rows x 128 bytes in the 128-byte swizzle (16-byte chunk c
 // of row r at c ^ (r & 7)), as the tiled copies write them.
@@ -105,7 +115,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
 }
 
 // e4m3 values enter the products as fp16, converted here (the type's own mma.sync
-// form converts both operands inside, one of them anew for every row tile).
+// form runs as two fp16 products and converts both operands inside, one of them
+// anew for every row tile: 4 drafted tokens on 2 x 131072 keys 199 us, so 172).
 // A 32-bit register of four e4m3 values gives two 16-bit operand registers, so
 // the products' k runs over the values (first product) or keys (second) in the
 // order 0 1 | 4 5 | 8 9 | 12 13 | 2 3 | 6 7 | 10 11 | 14 15 of each 16.  The queries
@@ -129,11 +140,12 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     const KParams& p = D.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    // warp = head of the group + hc * (which of the kw warps that share its units)
-    const int hs = warp % D.hc, kw = kWarps / D.hc;
+    // warp = head of the CTA + hw * (which of the kw warps that share its units)
+    const int hw = D.hw, hs = warp % hw, kw = kWarps / hw;
     uint8_t* const my_ring = ring + warp * V::RING;
     const uint32_t my_smem = smem_u32(my_ring);
-    const int c = blockIdx.x;
+    // adjacent CTAs take the heads of a group over the same keys
+    const int gp = D.hc / hw, c = blockIdx.x / gp, h0 = (blockIdx.x - c * gp) * hw;
     if (lane == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
         fence_mbar_init();
@@ -147,17 +159,17 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     wait_previous();
 
     Share share;  // a share is at least one unit of each warp
-    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.x, kw, true, share)) return;
+    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.x / gp, kw, h0 == 0, share)) return;
     const SeqInfo& s = share.s;
     Segment seg;
     while (next_segment<R, kUnit>(D, share, seg)) {
         const int b = share.b, group = seg.group, tile = seg.tile, rows = seg.rows;
-        const int hk = group * D.hc + hs;
+        const int hk = group * D.hc + h0 + hs;
         const int x0 = seg.x0, x1 = seg.x1, t_first = seg.t_first, t_last = seg.t_last;
         const int seen_all = seg.seen_all, seen_any = seg.seen_any;
 
         // ---- the copies of this warp: its units are kw apart ----
-        const int first = x0 + warp / D.hc;
+        const int first = x0 + warp / hw;
         const int steps = x1 > first ? (x1 - first + kw - 1) / kw : 0;
         // lane i: cache row where unit 32 k + i of this warp starts, and the
         // unit's factors; the next round of 32 units is on its way, unchecked
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         auto q_row = [&](int hx, int r) {
             const int i = tile * R + min(r, rows - 1);
             return static_cast<const uint8_t*>(D.q) +
-                   ((long long)(s.q0 + token_of(D, i)) * p.Hq + (group * D.hc + hx) * p.G + head_of(D, i)) * RB;
+                   ((long long)(s.q0 + token_of(D, i)) * p.Hq + (group * D.hc + h0 + hx) * p.G + head_of(D, i)) * RB;
         };
         uint32_t q_raw[V::Q_SMEM ? 1 : NT][FP8 ? QC : 2 * QC];
         float q_scale[NT][2], k_scale = 1.f;
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         if constexpr (V::Q_SMEM) {
             // [head][row][RB bytes], 16-byte chunk x at x ^ (row & 7) of each 8
             static_assert(!FP8, "16-bit queries");
-            for (int y = threadIdx.x; y < D.hc * R * (RB / 16); y += kThreads) {
+            for (int y = threadIdx.x; y < hw * R * (RB / 16); y += kThreads) {
                 const int ch = y % (RB / 16), r = y / (RB / 16) % R, hx = y / (RB / 16) / R;
                 *reinterpret_cast<uint4*>(q_smem + hx * V::Q_BYTES + r * RB + ((ch ^ (r & 7)) << 4)) =
                     *reinterpret_cast<const uint4*>(q_row(hx, r) + ch * 16);
@@ -500,27 +512,27 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         if (aborted) return;
         const bool whole = seg.whole();
         const int slot = 2 * c + (x0 == 0 ? 1 : 0);
-        for (int y = threadIdx.x; y < D.hc * rows * (DH / 4); y += kThreads) {
+        for (int y = threadIdx.x; y < hw * rows * (DH / 4); y += kThreads) {
             const int col = y % (DH / 4) * 4, r = y / (DH / 4) % rows, hx = y / (DH / 4) / rows;
             float M = -FLT_MAX, L = 0.f;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = hx; w < kWarps; w += D.hc) M = fmaxf(M, sm_m[w][r]);
-            for (int w = hx; w < kWarps; w += D.hc) {
+            for (int w = hx; w < kWarps; w += hw) M = fmaxf(M, sm_m[w][r]);
+            for (int w = hx; w < kWarps; w += hw) {
                 const float f = ex2(sm_m[w][r] - M);
                 L += f * sm_l[w][r];
                 O = plus(O, *reinterpret_cast<const float4*>(ring + w * V::RING + (r * OS + col) * 4), f);
             }
             if (whole) {
-                const int tok = token_of(D, tile * R + r), hkv = group * D.hc + hx, h = hkv * p.G + head_of(D, tile * R + r);
+                const int tok = token_of(D, tile * R + r), hkv = group * D.hc + h0 + hx, h = hkv * p.G + head_of(D, tile * R + r);
                 put_out(D, s.q0 + tok, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
                 if (D.lse && col == 0) D.lse[(long long)(s.q0 + tok) * p.Hq + h] = lse_of(M, L);
             } else {
-                const size_t at = ((size_t)slot * D.hc + hx) * R + r;
+                const size_t at = ((size_t)slot * D.hc + h0 + hx) * R + r;
                 *reinterpret_cast<float4*>(D.part + at * DH + col) = O;
                 if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(M, L);
             }
         }
-        if (threadIdx.x == 0) put_record(D, share, seg, c);
+        if (threadIdx.x == 0 && h0 == 0) put_record(D, share, seg, c);
         fence_proxy_async_smem();  // the ring held the warps' parts; copies come next
         __syncthreads();
         share.u = seg.item_at + x1;
@@ -602,7 +614,8 @@ __device__ __forceinline__ void finish_row(const DecodeParams& D, const Item& it
 constexpr int kJoinWarps = 16;
 
 // Few items, each of many parts: grid (items, hc * packed rows), a CTA per row,
-// whose warps add up every kJoinWarps-th part.
+// whose warps add up every kJoinWarps-th part.  5.6 us for 4 items of 111 parts, most
+// of them its launch and two loads that wait for one another.
 template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid_constant__ DecodeParams D) {
     constexpr int R = 8 * NT, E = DH / 32;
@@ -661,22 +674,27 @@ __global__ void __launch_bounds__(32 * kShareWarps) join_shares_kernel(const __g
 template <int DH, bool FP8, int NT>
 cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using V = Variant<DH, FP8, NT>;
-    // more than 8 packed rows at head dimension 128: whole tiles on the tensor core
+    // more than 16 packed rows at head dimension 128: tiles on the 5th-generation tensor
+    // core (4 tokens x 8 heads on 2 x 131072 e4m3 keys: 102 us, here 169; but 16 rows
+    // on 32768 bf16 keys: 65 us, here 53, and more so below)
     constexpr bool TILES = DH == 128 && NT == 4;
     // (at least one: lengths above a limit of 0 have to be recorded)
     const int packed = D.p.max_seqlen_q > 0 ? D.p.max_seqlen_q * D.p.G : 1;
-    D.hc = D.p.Hkv % kDecHeads ? 1 : kDecHeads;
+    // KV heads of an item: those whose rows of a token are 1 KB together, two of them in
+    // a CTA where warps take its products, the others in the CTAs beside it
+    D.hw = TILES || D.p.Hkv % 2 ? 1 : 2;
+    D.hc = kHeadBytes / V::RB;
+    while (D.p.Hkv % D.hc || D.hc % D.hw) --D.hc;
     D.groups = D.p.Hkv / D.hc;
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
-    D.few = items <= 64 && D.p.num_seqs <= kThreads;
-    int shares;
+    const int shares = (TILES ? decode_tile_ctas(FP8) : V::CTAS) / (D.hc / D.hw);
+    // join by item where they are long: their parts are shared out over 16 warps a row
+    D.few = items * 4 <= shares && D.p.num_seqs <= kThreads;
     cudaError_t e;
     if constexpr (TILES) {
-        shares = decode_tile_shares(D);
         e = launch_decode_tiles(D, s);
     } else {
-        shares = V::CTAS;
         static std::atomic<unsigned long long> ready{0};
         e = allow_smem(decode_kernel<DH, FP8, NT>, V::SMEM, ready);
         if (e != cudaSuccess) return e;

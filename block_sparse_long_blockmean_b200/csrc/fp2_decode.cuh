@@ -222,6 +222,6 @@ __device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b 
 // Multi-token tiles of head dimension 128 (fp2_decode_tiles.cu): the shares'
 // partial rows and records, as decode_kernel leaves them for 32 rows a tile.
 cudaError_t launch_decode_tiles(const DecodeParams& D, cudaStream_t s);
-int decode_tile_shares(const DecodeParams& D);
+int decode_tile_ctas(bool fp8);
 
 }  // namespace fp2

@@ -27,6 +27,12 @@
 // Warpgroups of four warps take the softmax, a thread a key; one more warp copies,
 // one issues the products.  They meet in mbarriers only, so that the copies run on
 // into the next segment.
+//
+// Bound by the cache's bytes and, 11 us above them, by the softmax's instructions: 4
+// tokens x 8 heads on 2 x 131072 e4m3 keys with factors (537 MB) 102 us, 5.3 TB/s; the
+// copies and products alone, with no softmax, 93.  A run of seconds reaches the power
+// limit and 1.73 GHz: 116 us.  K and V in one ring: 133 us (a value's place stays
+// taken until its product, a key's only until its logits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,7 +52,8 @@ struct Tile {
     static constexpr int HALF = kTileKeys * 128;          // bytes of one
     static constexpr int STAGE = HALVES * HALF;           // a tile of K or of V
     // e4m3 tiles arrive faster than a warpgroup takes their softmax: two CTAs on each
-    // SM.  bf16 stages leave room for one, whose rows two warpgroups share.
+    // SM (133 us; one, whose rows two warpgroups share, 141).  bf16 stages leave room for
+    // one CTA, and two warpgroups help it (4 x 32768 keys: 52 us, one warpgroup 68).
     static constexpr int PER_SM = FP8 ? 2 : 1;
     static constexpr int WGS = FP8 ? 1 : 2;               // softmax warpgroups
     static constexpr int H = kTileRows / WGS;             // rows of one
@@ -533,12 +540,13 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             }
             tc_fence_after();
             float o[H];
-#pragma unroll
-            for (int k = 0; k < C::TERMS; ++k) {
+            tmem_load(tmem + lanes + C::O_COL + first, o);
+#pragma unroll 1
+            for (int k = 1; k < C::TERMS; ++k) {
                 float y[H];
                 tmem_load(tmem + lanes + C::O_COL + k * R + first, y);
 #pragma unroll
-                for (int i = 0; i < H; ++i) o[i] = k ? o[i] + y[i] : y[i];
+                for (int i = 0; i < H; ++i) o[i] += y[i];
             }
             tc_fence_before();
             const float sum_of = reduce_rows<H>(l, [](float a, float b) { return a + b; });
@@ -577,45 +585,40 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             if (to > from) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) o[i] *= sm_f[first + i];
+#pragma unroll 1
                 for (int k = from; k < to; ++k) {
                     float v;
                     if constexpr (FP8) v = e4m3_pair(sm_tv[k][tid]).x;
                     else v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sm_tv[k])[tid]);
-                    const int j = g.seen_all + k;
+                    // the rows of this warpgroup that see the key, from the first one on
+                    const int sees = ((g.seen_all + k - s.P) << D.g_shift) - g.tile * R - first;
 #pragma unroll
                     for (int i = 0; i < H; ++i)
-                        if (first + i < g.rows && j <= s.P + token(first + i)) o[i] = fmaf(sm_w[k][first + i], v, o[i]);
+                        if (i >= sees) o[i] = fmaf(sm_w[k][first + i], v, o[i]);
                 }
             }
-            const int slot = 2 * c + (g.x0 == 0 ? 1 : 0);
+            // through the weights' place in shared memory (its last reader is done, and the
+            // next writer waits for all warpgroups' queries): short code, four columns a store
+            float* const rows = reinterpret_cast<float*>(smem + C::OFF_P) + first * DH;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int r = first + i;
-                if (r >= g.rows) break;
+            for (int i = 0; i < H; ++i) rows[i * DH + tid] = o[i];
+            softmax_sync(wg);
+            const int slot = 2 * c + (g.x0 == 0 ? 1 : 0);
+#pragma unroll 1
+            for (int y = tid; y < min(H, g.rows - first) * (DH / 4); y += 128) {
+                const int col = y % (DH / 4) * 4, r = first + y / (DH / 4);
+                const float4 O = *reinterpret_cast<const float4*>(&rows[(r - first) * DH + col]);
                 if (g.whole()) {
-                    const float y = o[i] * ((FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]);
-                    const long long at = ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * DH + tid;
-                    if (p.out_fp8) {
-                        const float unit = p.out_scale ? p.out_scale[head(r)] : p.v_scale[hk];
-                        static_cast<uint8_t*>(D.out)[at] = (uint8_t)pack_e4m3x4(y / unit, 0.f, 0.f, 0.f);
-                    } else {
-                        static_cast<__nv_bfloat16*>(D.out)[at] = __float2bfloat16(y);
-                    }
-                } else {
-                    D.part[(((size_t)slot * D.hc + hs) * R + r) * DH + tid] = o[i];
-                }
-            }
-            if (tid < H && first + tid < g.rows) {
-                const int r = first + tid;
-                if (g.whole()) {
-                    if (D.lse) D.lse[(long long)(s.q0 + token(r)) * p.Hq + head(r)] = lse_of(sm_m[r], sm_l[r]);
+                    put_out(D, s.q0 + token(r), head(r), col, scaled(O, (FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]));
+                    if (D.lse && col == 0) D.lse[(long long)(s.q0 + token(r)) * p.Hq + head(r)] = lse_of(sm_m[r], sm_l[r]);
                 } else {
                     const size_t at = ((size_t)slot * D.hc + hs) * R + r;
-                    *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[r], sm_l[r]);
+                    *reinterpret_cast<float4*>(D.part + at * DH + col) = O;
+                    if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[r], sm_l[r]);
                 }
             }
             if (threadIdx.x == 0 && hs == 0) put_record(D, x, g, c);
-            softmax_sync(wg);  // sm_* are free for the next segment
+            softmax_sync(wg);  // sm_* and P are free for the next segment
             x.u = g.item_at + g.x1;
         }
         if (dead && lane == 0) set_error(p.err, kErrTimeout, kDetTileSoftmax);
@@ -646,6 +649,6 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
 cudaError_t launch_decode_tiles(const DecodeParams& D, cudaStream_t s) {
     return D.p.fp8 ? launch<true>(D, s) : launch<false>(D, s);
 }
-int decode_tile_shares(const DecodeParams& D) { return (D.p.fp8 ? Tile<true>::CTAS : Tile<false>::CTAS) / D.hc; }
+int decode_tile_ctas(bool fp8) { return fp8 ? Tile<true>::CTAS : Tile<false>::CTAS; }
 
 }  // namespace fp2

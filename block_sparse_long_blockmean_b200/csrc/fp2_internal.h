@@ -117,13 +117,13 @@ struct DecodeParams {
     float* part_ml;
     int4* record;              // [kDecCtas][2]: what the join kernel has to do
     float qk_scale;            // log2(e) / sqrt(d)
-    // set by the launchers: KV heads of an item, groups of them, row tiles of the
-    // longest sequence, records by item (few items) or by share
-    int hc, groups, tiles_max, few;
+    // set by the launchers: KV heads of an item, those of one CTA of it, groups of
+    // heads, row tiles of the longest sequence, records by item (few) or by share
+    int hc, hw, groups, tiles_max, few;
     int g_shift;               // log2 of the query heads of a KV head
     int box;                   // rows of a copy of the tile kernel
 };
-constexpr int kDecHeads = 2;   // most KV heads of an item
+constexpr int kDecHeads = 2;   // most KV heads of a CTA
 constexpr int kDecCtas = 444;  // most CTAs of the split: 3 on each of 148 SMs
 constexpr int kDecRows = 32;   // most packed query rows (tokens x group heads) of a tile
 

@@ -6,6 +6,9 @@
 // likewise.  Every CTA takes both sums over all sequences for itself, in shared
 // memory (they are a few KB and come from L2), and then maps its share of the
 // tokens and pages by binary search, so that no CTA waits for another.
+//
+// Bound by its launch and three loads that wait for one another: 64 sequences of one
+// token 2.9 us, 1000 of up to 511 tokens 5.2, 8 of 32768 3.8 (2.1 MB: 0.3 us of bytes).
 #include "fp2_device.cuh"
 #include "fp2_launch.cuh"
 
