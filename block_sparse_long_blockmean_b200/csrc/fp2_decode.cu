@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(M, L);
             }
         }
-        if (threadIdx.x == 0 && h0 == 0) put_record(D, share, seg, c);
+        if (threadIdx.x == 0 && h0 == 0) put_record(D, share, s.q0, b, seg, c);
         fence_proxy_async_smem();  // the ring held the warps' parts; copies come next
         __syncthreads();
         share.u = seg.item_at + x1;

@@ -193,11 +193,11 @@ __device__ __forceinline__ bool next_segment(const DecodeParams& D, Share& x, Se
     return true;
 }
 // One thread: what the join has to do for an item that starts in this segment.
-__device__ __forceinline__ void put_record(const DecodeParams& D, const Share& x, const Segment& g, int c) {
+__device__ __forceinline__ void put_record(const DecodeParams& D, const Share& x, int q0, int b, const Segment& g, int c) {
     if (g.x0 != 0 || !(D.few || !g.whole())) return;
     const int parts = g.whole() ? 0 : x.of_unit(g.item_at + g.per_item - 1) - c + 1;
-    const int at = 2 * (D.few ? (x.b * D.groups + g.group) * D.tiles_max + g.tile : c);
-    D.record[at] = make_int4(parts, x.s.q0, g.group, g.tile);
+    const int at = 2 * (D.few ? (b * D.groups + g.group) * D.tiles_max + g.tile : c);
+    D.record[at] = make_int4(parts, q0, g.group, g.tile);
     D.record[at + 1] = make_int4(g.rows, c, 0, 0);
 }
 

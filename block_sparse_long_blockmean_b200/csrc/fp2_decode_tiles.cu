@@ -73,7 +73,7 @@ struct Tile {
     static_assert(O_COL + PV_N <= (int)TMEM && PER_SM * (SMEM + 9 * 1024) <= 228 * 1024, "on-chip memory");
 };
 
-enum { T_K_FULL = 0, T_K_EMPTY = 3, T_V_FULL = 6, T_V_EMPTY = 9, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_TAIL, T_DRAIN, T_COUNT };
+enum { T_K_FULL = 0, T_K_EMPTY = 3, T_V_FULL = 6, T_V_EMPTY = 9, T_S_FULL = 12, T_S_FREE = 14, T_P_READY = 16, T_O_DONE = 18, T_Q_READY = 20, T_MEET, T_DRAIN, T_COUNT };
 enum { kDetTileCopy = kDetWaitBase + 8, kDetTileMma, kDetTileSoftmax };
 
 // Instruction descriptor with fp32 accumulation: operand formats a, b (kind::f16:
@@ -94,22 +94,11 @@ __device__ __forceinline__ bool softmax_any(int wg, bool x) {
     return r != 0;
 }
 
-// The reduction of v[i] over the warp's lanes: in lane i of 32 rows, in lanes 2 i
-// and 2 i + 1 of 16.
-template <int H, typename Op>
-__device__ __forceinline__ float reduce_rows(float (&v)[H], Op op) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int half = H / 2; half > 0; half >>= 1) {
-        const int mask = half * (32 / H);
-        const bool up = lane & mask;
-#pragma unroll
-        for (int i = 0; i < half; ++i) {
-            const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(~0u, send, mask));
-        }
-    }
-    return H == 32 ? v[0] : op(v[0], __shfl_xor_sync(~0u, v[0], 1));
+// The largest of a value over the warp's lanes, in all of them.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // 32 lanes x 16 consecutive 32-bit TMEM columns.
@@ -162,7 +151,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
-            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY || i == T_TAIL ? 4 * WGS : 1);
+            mbar_init(&bars[i], (i >= T_S_FREE && i < T_O_DONE) || i == T_Q_READY || i == T_MEET ? 4 * WGS : 1);
         fence_mbar_init();
         aborted = 0;
         prefetch_tmap(&maps.k);
@@ -319,24 +308,145 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
         // the product of tile i has read its weights and values
         auto product_done = [&](int i) { return mbar_wait(&bars[T_O_DONE + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs); };
         bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
-        int tails = 0;                 // segments with keys set aside
-        while (!dead && next_segment<R, kTileKeys>(D, x, g)) {
-            const SeqInfo& s = x.s;
-            const int hk = g.group * D.hc + hs, n_tiles = g.x1 - g.x0;
-            auto token = [&](int r) { return token_of(D, g.tile * R + r); };
-            auto head = [&](int r) { return hk * p.G + head_of(D, g.tile * R + r); };
-            auto q_row = [&](int r) {
-                return static_cast<const uint8_t*>(D.q) + ((long long)(s.q0 + token(r)) * p.Hq + head(r)) * RB;
-            };
-            for (int i = tid; i < H * RB / 16; i += 128) {  // Q tile, swizzled, rows past the last 0
-                const int r = first + i / (RB / 16), ch = i % (RB / 16);
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r < g.rows) v = *reinterpret_cast<const uint4*>(q_row(r) + ch * 16);
-                *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * R * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+        int meets = 0;                 // of the two warpgroups
+        auto meet = [&] {
+            arrive(&bars[T_MEET]);
+            ok = mbar_wait(&bars[T_MEET], meets++ & 1, &aborted, kDecWaitNs) && ok;
+            __syncwarp();
+        };
+        SeqInfo s;                     // of the segment in hand
+        int b = 0, hk = 0, n_tiles = 0;
+        float l[H];
+        auto token = [&](int r) { return token_of(D, g.tile * R + r); };
+        auto head = [&](int r) { return hk * p.G + head_of(D, g.tile * R + r); };
+        for (bool begun = false;; begun = true) {
+            // the next segment's queries before this one's result: their place is free, all
+            // logits are there, and the products go on meanwhile
+            Segment next;
+            const bool more = next_segment<R, kTileKeys>(D, x, next);
+            if (more) {
+                const int head0 = (next.group * D.hc + hs) * p.G;
+                for (int i = tid; i < H * RB / 16; i += 128) {  // swizzled, rows past the last 0
+                    const int r = first + i / (RB / 16), ch = i % (RB / 16), at = next.tile * R + r;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < next.rows)
+                        v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(D.q) + ch * 16 +
+                                                            ((long long)(x.s.q0 + token_of(D, at)) * p.Hq + head0 + head_of(D, at)) * RB);
+                    *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * R * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                arrive(&bars[T_Q_READY]);
             }
-            fence_proxy_async_smem();
-            arrive(&bars[T_Q_READY]);
-            float l[H];
+            if (begun) {
+                // ------------------------------------------ the segment's result ---
+                // (code that runs once or twice is fetched as it runs, at 30 cycles an
+                // instruction: what can be is a loop here)
+                ok = product_done(t - 1) && ok;
+                __syncwarp();
+                if (softmax_any(wg, !ok)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                float o[H];
+                tmem_load(tmem + lanes + C::O_COL + first, o);
+#pragma unroll 1
+                for (int k = 1; k < C::TERMS; ++k) {
+                    float y[H];
+                    tmem_load(tmem + lanes + C::O_COL + k * R + first, y);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) o[i] += y[i];
+                }
+                tc_fence_before();
+                // the weights' place in shared memory takes the rows: its last reader is done
+                float* const rows = reinterpret_cast<float*>(smem + C::OFF_P) + first * DH;
+#pragma unroll
+                for (int i = 0; i < H; ++i) rows[i * DH + tid] = l[i];
+                // the keys set aside in this segment: [from, to) of them
+                const int from = max(0, g.x0 * kTileKeys - g.seen_all);
+                const int to = min(g.seen_any, g.x1 * kTileKeys) - g.seen_all;
+                softmax_sync(wg);
+                if (WGS > 1 && to > from) {  // (the other warpgroup holds half of the values)
+                    meet();
+                    if (softmax_any(wg, !ok)) {
+                        dead = true;
+                        break;
+                    }
+                }
+                {
+                    constexpr int TPR = 128 / H;  // threads that add up a row, H keys each
+                    const int r = first + tid / TPR;
+                    float sum = 0.f;
+#pragma unroll 2
+                    for (int i = 0; i < H; i += 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(&rows[tid * H + (i + tid * 4) % H]);
+                        sum += (y.x + y.y) + (y.z + y.w);
+                    }
+#pragma unroll
+                    for (int i = 1; i < TPR; i <<= 1) sum += __shfl_xor_sync(~0u, sum, i);
+                    if (tid % TPR == 0) {
+                        const float m = -sm_nm[r];
+                        float most = m;
+                        for (int k = from; k < to; ++k) most = fmaxf(most, sm_w[k][r]);
+                        const float f = ex2(m - most);
+                        sum *= f;
+#pragma unroll 1
+                        for (int k = from; k < to; ++k) {
+                            const float w = ex2(sm_w[k][r] - most);
+                            sum += w;
+                            sm_w[k][r] = FP8 ? w * sm_tf[k] : w;
+                        }
+                        sm_m[r] = most;
+                        sm_l[r] = sum;
+                        sm_f[r] = f;
+                    }
+                }
+                softmax_sync(wg);
+#pragma unroll
+                for (int i = 0; i < H; ++i) rows[i * DH + tid] = o[i];
+                softmax_sync(wg);
+                const int slot = 2 * c + (g.x0 == 0 ? 1 : 0);
+#pragma unroll 1
+                for (int y = tid; y < min(H, g.rows - first) * (DH / 4); y += 128) {
+                    const int col = y % (DH / 4) * 4, r = first + y / (DH / 4);
+                    float4 O = scaled(*reinterpret_cast<const float4*>(&rows[(r - first) * DH + col]), sm_f[r]);
+                    // the keys set aside that the row sees: the row's token is the last
+                    const int seen_to = min(to, token(r) - g.t_first);
+#pragma unroll 1
+                    for (int k = from; k < seen_to; ++k) {
+                        const uint8_t* v = sm_tv[k] + col * (FP8 ? 1 : 2);
+                        float4 V;
+                        if constexpr (FP8) {
+                            const uint32_t u = *reinterpret_cast<const uint32_t*>(v);
+                            const float2 lo = e4m3_pair((uint16_t)u), hi = e4m3_pair((uint16_t)(u >> 16));
+                            V = make_float4(lo.x, lo.y, hi.x, hi.y);
+                        } else {
+                            const uint2 u = *reinterpret_cast<const uint2*>(v);
+                            V = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                                            __uint_as_float(u.y & 0xFFFF0000u));
+                        }
+                        O = plus(O, V, sm_w[k][r]);
+                    }
+                    if (g.whole()) {
+                        put_out(D, s.q0 + token(r), head(r), col, scaled(O, (FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]));
+                        if (D.lse && col == 0) D.lse[(long long)(s.q0 + token(r)) * p.Hq + head(r)] = lse_of(sm_m[r], sm_l[r]);
+                    } else {
+                        const size_t at = ((size_t)slot * D.hc + hs) * R + r;
+                        *reinterpret_cast<float4*>(D.part + at * DH + col) = O;
+                        if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[r], sm_l[r]);
+                    }
+                }
+                if (threadIdx.x == 0 && hs == 0) put_record(D, x, s.q0, b, g, c);
+                // sm_* and P are free for the next segment
+                if constexpr (WGS > 1) meet();
+                else softmax_sync(wg);
+            }
+            if (!more) break;
+            g = next;
+            s = x.s;
+            b = x.b;
+            hk = g.group * D.hc + hs;
+            n_tiles = g.x1 - g.x0;
 #pragma unroll
             for (int i = 0; i < H; ++i) l[i] = 0.f;
             if (tid < H) {
@@ -347,7 +457,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             softmax_sync(wg);
             auto factors = [&](int n) {  // of tile n's key block; used a tile later
                 if (!FP8 || !p.kb_fac || n >= n_tiles) return make_float2(1.f, 1.f);
-                const size_t at = ((size_t)x.b * p.nkb_max + g.x0 + n) * p.Hkv + hk;
+                const size_t at = ((size_t)b * p.nkb_max + g.x0 + n) * p.Hkv + hk;
                 return make_float2(p.kb_fac[at], p.vb_fac[at]);
             };
             float2 fac_next = factors(0);
@@ -398,8 +508,13 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     tmem_load(s_at, w);
 #pragma unroll
                     for (int i = 0; i < H; ++i) w[i] = seen ? w[i] * factor(i) : -INFINITY;
-                    const float top_of = reduce_rows<H>(w, [](float a, float b) { return fmaxf(a, b); });
-                    red[w4][H == 32 ? lane : lane >> 1] = top_of;
+                    float top_of = 0.f;  // row `lane`'s
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float y = warp_max(w[i]);
+                        if (lane == i) top_of = y;
+                    }
+                    if (lane < H) red[w4][lane] = top_of;
                     softmax_sync(wg);
                     if (tid < H) {
                         const float most = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
@@ -530,95 +645,6 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                 arrive(&bars[T_P_READY + (t & 1)]);
             }
             if (dead) break;
-
-            // ------------------------------------------- the segment's result ---
-            ok = product_done(t - 1) && ok;
-            __syncwarp();
-            if (softmax_any(wg, !ok)) {
-                dead = true;
-                break;
-            }
-            tc_fence_after();
-            float o[H];
-            tmem_load(tmem + lanes + C::O_COL + first, o);
-#pragma unroll 1
-            for (int k = 1; k < C::TERMS; ++k) {
-                float y[H];
-                tmem_load(tmem + lanes + C::O_COL + k * R + first, y);
-#pragma unroll
-                for (int i = 0; i < H; ++i) o[i] += y[i];
-            }
-            tc_fence_before();
-            const float sum_of = reduce_rows<H>(l, [](float a, float b) { return a + b; });
-            red[w4][H == 32 ? lane : lane >> 1] = sum_of;
-            // the keys set aside in this segment: [from, to) of them
-            const int from = max(0, g.x0 * kTileKeys - g.seen_all);
-            const int to = min(g.seen_any, g.x1 * kTileKeys) - g.seen_all;
-            softmax_sync(wg);
-            if (WGS > 1 && to > from) {  // (the other warpgroup holds half of the values)
-                arrive(&bars[T_TAIL]);
-                ok = mbar_wait(&bars[T_TAIL], tails & 1, &aborted, kDecWaitNs);
-                __syncwarp();
-                ++tails;
-                if (softmax_any(wg, !ok)) {
-                    dead = true;
-                    break;
-                }
-            }
-            if (tid < H) {
-                const int r = first + tid;
-                const float m = -sm_nm[r];
-                float most = m, sum = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
-                for (int k = from; k < to; ++k) most = fmaxf(most, sm_w[k][r]);
-                const float f = ex2(m - most);
-                sum *= f;
-                for (int k = from; k < to; ++k) {
-                    const float w = ex2(sm_w[k][r] - most);
-                    sum += w;
-                    sm_w[k][r] = FP8 ? w * sm_tf[k] : w;
-                }
-                sm_m[r] = most;
-                sm_l[r] = sum;
-                sm_f[r] = f;
-            }
-            softmax_sync(wg);
-            if (to > from) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) o[i] *= sm_f[first + i];
-#pragma unroll 1
-                for (int k = from; k < to; ++k) {
-                    float v;
-                    if constexpr (FP8) v = e4m3_pair(sm_tv[k][tid]).x;
-                    else v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sm_tv[k])[tid]);
-                    // the rows of this warpgroup that see the key, from the first one on
-                    const int sees = ((g.seen_all + k - s.P) << D.g_shift) - g.tile * R - first;
-#pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        if (i >= sees) o[i] = fmaf(sm_w[k][first + i], v, o[i]);
-                }
-            }
-            // through the weights' place in shared memory (its last reader is done, and the
-            // next writer waits for all warpgroups' queries): short code, four columns a store
-            float* const rows = reinterpret_cast<float*>(smem + C::OFF_P) + first * DH;
-#pragma unroll
-            for (int i = 0; i < H; ++i) rows[i * DH + tid] = o[i];
-            softmax_sync(wg);
-            const int slot = 2 * c + (g.x0 == 0 ? 1 : 0);
-#pragma unroll 1
-            for (int y = tid; y < min(H, g.rows - first) * (DH / 4); y += 128) {
-                const int col = y % (DH / 4) * 4, r = first + y / (DH / 4);
-                const float4 O = *reinterpret_cast<const float4*>(&rows[(r - first) * DH + col]);
-                if (g.whole()) {
-                    put_out(D, s.q0 + token(r), head(r), col, scaled(O, (FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]));
-                    if (D.lse && col == 0) D.lse[(long long)(s.q0 + token(r)) * p.Hq + head(r)] = lse_of(sm_m[r], sm_l[r]);
-                } else {
-                    const size_t at = ((size_t)slot * D.hc + hs) * R + r;
-                    *reinterpret_cast<float4*>(D.part + at * DH + col) = O;
-                    if (col == 0) *reinterpret_cast<float2*>(D.part_ml + at * 2) = make_float2(sm_m[r], sm_l[r]);
-                }
-            }
-            if (threadIdx.x == 0 && hs == 0) put_record(D, x, g, c);
-            softmax_sync(wg);  // sm_* and P are free for the next segment
             x.u = g.item_at + g.x1;
         }
         if (dead && lane == 0) set_error(p.err, kErrTimeout, kDetTileSoftmax);
