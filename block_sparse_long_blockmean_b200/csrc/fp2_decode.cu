@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = kDecBox;  // keys of a unit: one copy
-constexpr int kHeadBytes = 1024;  // of the heads' rows of a token that are read together
+constexpr int kHeadBytes = 2048;  // of the heads' rows of a token that are read together
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
 // Four warps a CTA, each with a ring of its own: a CTA of 8 warps on each SM leaves it
