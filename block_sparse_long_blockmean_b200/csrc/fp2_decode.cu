@@ -36,7 +36,7 @@ namespace fp2 {
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;  // (4: a CTA of hw = 1, 2 heads has 1 << (3 - hw) warps a head)
 constexpr int kUnit = kDecBox;  // keys of a unit: one copy
 constexpr int kHeadBytes = 2048;  // of the heads' rows of a token that are read together
 
@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     // warp = head of the CTA + hw * (which of the kw warps that share its units)
-    const int hw = D.hw, hs = warp % hw, kw = kWarps / hw;
+    const int hw = D.hw, hs = warp & (hw - 1), kw = kWarps >> (hw - 1);
     uint8_t* const my_ring = ring + warp * V::RING;
     const uint32_t my_smem = smem_u32(my_ring);
     // adjacent CTAs take the heads of a group over the same keys
-    const int gp = D.hc / hw, c = blockIdx.x / gp, h0 = (blockIdx.x - c * gp) * hw;
+    const int c = blockIdx.y, h0 = blockIdx.x * hw;
     if (lane == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
         fence_mbar_init();
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     wait_previous();
 
     Share share;  // a share is at least one unit of each warp
-    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.x / gp, kw, h0 == 0, share)) return;
-    const SeqInfo& s = share.s;
+    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.y, kw, h0 == 0, share)) return;
+    const Lens& s = share.s;
     Segment seg;
     while (next_segment<R, kUnit>(D, share, seg)) {
         const int b = share.b, group = seg.group, tile = seg.tile, rows = seg.rows;
@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         const int seen_all = seg.seen_all, seen_any = seg.seen_any;
 
         // ---- the copies of this warp: its units are kw apart ----
-        const int first = x0 + warp / hw;
-        const int steps = x1 > first ? (x1 - first + kw - 1) / kw : 0;
+        const int first = x0 + (warp >> (hw - 1));
+        const int steps = x1 > first ? (x1 - first + kw - 1) >> (3 - hw) : 0;
         // lane i: cache row where unit 32 k + i of this warp starts, and the
         // unit's factors; the next round of 32 units is on its way, unchecked
         int row_now = -1, raw_next = 0;
@@ -179,14 +179,14 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         auto fetch_round = [&](int n0) {
             const int n = n0 + lane;
             if (n >= steps) return;
-            raw_next = raw_row(p, s, b, key_at(n));
+            raw_next = raw_row(D, s, b, key_at(n));
             if (FP8 && p.kb_fac) {
-                const size_t f = ((size_t)b * p.nkb_max + key_at(n) / p.B) * p.Hkv + hk;
+                const size_t f = ((size_t)b * p.nkb_max + key_at(n) / kFactorKeys) * p.Hkv + hk;
                 fac_next = make_float2(p.kb_fac[f], p.vb_fac[f]);
             }
         };
         auto begin_round = [&](int n0) {
-            row_now = n0 + lane < steps ? checked_row(p, raw_next, key_at(n0 + lane)) : -1;
+            row_now = n0 + lane < steps ? checked_row(D, raw_next, key_at(n0 + lane)) : -1;
             fac_now = fac_next;
             if (FP8 && p.kb_fac && !(fac_now.x > 0.f && fac_now.x <= 1.f && fac_now.y > 0.f && fac_now.y <= 1.f)) {
                 set_error(p.err, kErrInvalid, kDetFactor);
@@ -702,7 +702,7 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
         // L2 fetches in pieces of 256 bytes where the item reads both halves
         const bool wide = D.hc * V::RB >= 256 || D.p.Hkv == 1;
         if (!make_row_maps(D.p, D.k, D.v, kUnit, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
-        e = launch_early(decode_kernel<DH, FP8, NT>, dim3(V::CTAS), kThreads, V::SMEM, s, D, maps);
+        e = launch_early(decode_kernel<DH, FP8, NT>, dim3(D.hc / D.hw, shares), kThreads, V::SMEM, s, D, maps);
     }
     if (e != cudaSuccess) return e;
     if (D.few)

@@ -10,6 +10,7 @@
 namespace fp2 {
 
 constexpr uint64_t kDecWaitNs = 2000000000ull;  // 2 s per wait for a copy or a product
+constexpr int kFactorKeys = 128;                // keys that share their scale factors (e4m3's only block)
 constexpr int kDecBox = 16;                     // rows of a copy: they never cross a page
 
 // Weights are taken relative to m = (largest z when m was set) - kLift and may
@@ -22,13 +23,25 @@ struct DecodeMaps {
     CUtensorMap k, v;  // [rows][Hkv][d], boxes of some rows x 128 bytes of one head
 };
 
+// A sequence's lengths, as far as they matter here.  (Code before the first copy counts:
+// it is fetched as it runs, at about 30 cycles an instruction.)
+struct Lens {
+    int q0, Lq, Lk, k0, P;
+};
+__device__ __forceinline__ bool load_lens(const DecodeParams& D, int b, Lens& s) {
+    SeqInfo x;
+    const bool ok = load_seq(D.p, b, x);
+    s = {x.q0, x.Lq, x.Lk, x.k0, x.P};
+    return ok;
+}
+
 struct Shape {
     long long units;  // of the sequence
     int per_item;     // units of one item: ceil(Lk / UNIT)
     int tiles;        // row tiles per head group
 };
 template <int R, int UNIT>
-__device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const SeqInfo& s) {
+__device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const Lens& s) {
     Shape x;
     x.per_item = (s.Lk + UNIT - 1) / UNIT;
     x.tiles = ((s.Lq << D.g_shift) + R - 1) / R;
@@ -37,8 +50,8 @@ __device__ __forceinline__ Shape seq_shape(const DecodeParams& D, const SeqInfo&
 }
 // Sequence b's lengths and its units; 0 units if it rests or its lengths are bad.
 template <int R, int UNIT>
-__device__ __forceinline__ long long seq_units(const DecodeParams& D, int b, SeqInfo& s) {
-    if (!load_seq(D.p, b, s) || s.Lq == 0) return 0;
+__device__ __forceinline__ long long seq_units(const DecodeParams& D, int b, Lens& s) {
+    if (!load_lens(D, b, s) || s.Lq == 0) return 0;
     return seq_shape<R, UNIT>(D, s).units;
 }
 // Packed row i of a sequence and KV head: its token, its query head within the group.
@@ -52,16 +65,16 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 
 // Cache row of key `key` in two steps, so that a page id can be on its way while
 // other work is done: what has to be loaded, and the row, -1 (recorded) if it is bad.
-__device__ __forceinline__ int raw_row(const KParams& p, const SeqInfo& s, int b, int key) {
-    return p.paged ? p.page_table[(size_t)b * p.max_pages + key / p.page_size] : s.k0 + key;
+__device__ __forceinline__ int raw_row(const DecodeParams& D, const Lens& s, int b, int key) {
+    return D.p.paged ? D.p.page_table[(size_t)b * D.p.max_pages + (key >> D.page_shift)] : s.k0 + key;
 }
-__device__ __forceinline__ int checked_row(const KParams& p, int raw, int key) {
-    if (!p.paged) return raw;
-    if (raw < 0 || raw >= p.num_pages) {
-        set_error(p.err, kErrBounds, kDetPage);
+__device__ __forceinline__ int checked_row(const DecodeParams& D, int raw, int key) {
+    if (!D.p.paged) return raw;
+    if (raw < 0 || raw >= D.p.num_pages) {
+        set_error(D.p.err, kErrBounds, kDetPage);
         return -1;
     }
-    return raw * p.page_size + key % p.page_size;
+    return (raw << D.page_shift) + (key & (D.p.page_size - 1));
 }
 
 // Sum of x over the CTA of W warps and the exclusive prefix of the calling thread.
@@ -94,7 +107,7 @@ __device__ __forceinline__ long long block_prefix(long long x, long long& total,
 struct Share {
     long long total, u, u_end, seq_at;
     int parts, b;
-    SeqInfo s;
+    Lens s;
     __device__ __forceinline__ long long start(int i) const { return quotient(total * i, parts); }
     // the last share that an item reaches whose last unit is `end`: the largest i
     // with start(i) <= end, that is total i < (end + 1) parts
@@ -107,13 +120,13 @@ __device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int sha
     __shared__ long long chunk_end;
     const KParams& p = D.p;
     constexpr int T = 32 * W;
-    SeqInfo s;
+    Lens s;
     long long total = 0, n = (int)threadIdx.x < p.num_seqs ? seq_units<R, UNIT>(D, threadIdx.x, s) : 0;
     long long at = block_prefix<W>(n, total, sums);
     for (int b0 = T; b0 < p.num_seqs; b0 += T) {
         const int b = b0 + threadIdx.x;
         long long t;
-        SeqInfo y;
+        Lens y;
         block_prefix<W>(b < p.num_seqs ? seq_units<R, UNIT>(D, b, y) : 0, t, sums);
         total += t;
     }
@@ -175,7 +188,7 @@ __device__ __forceinline__ bool next_segment(const DecodeParams& D, Share& x, Se
         x.seq_at += sh.units;
         do
             if (++x.b >= p.num_seqs) return false;
-        while (!load_seq(p, x.b, x.s) || x.s.Lq == 0);
+        while (!load_lens(D, x.b, x.s) || x.s.Lq == 0);
         sh = seq_shape<R, UNIT>(D, x.s);
     }
     const int item = (int)quotient(x.u - x.seq_at, sh.per_item);

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // adjacent CTAs take the heads of a group over the same keys, so that a token's
     // rows of both are read at about the same time
-    const int c = blockIdx.x / D.hc, hs = blockIdx.x % D.hc;
+    const int c = blockIdx.y, hs = blockIdx.x;
     const uint32_t base = smem_u32(smem);
     if (threadIdx.x == 0) {
         for (int i = 0; i < T_COUNT; ++i)
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     }
     wait_previous();
     Share x;
-    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.x / D.hc, 1, hs == 0, x)) return;
+    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.y, 1, hs == 0, x)) return;
     if (warp == MMA_WARP) {
         tmem_alloc(&tmem_at, C::TMEM);
         tmem_relinquish();
@@ -184,11 +184,11 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             auto wanted = [&](int n) {
                 return n + (lane >> 3) < n_tiles && (lane & 7) * D.box < kTileKeys && key_of(n) < g.seen_any;
             };
-            int now = -1, next = wanted(0) ? raw_row(p, x.s, x.b, key_of(0)) : 0;
+            int now = -1, next = wanted(0) ? raw_row(D, x.s, x.b, key_of(0)) : 0;
             for (int n = 0; n < n_tiles; ++n, ++t) {
                 if ((n & 3) == 0) {
-                    now = wanted(n) ? checked_row(p, next, key_of(n)) : -1;
-                    if (wanted(n + 4)) next = raw_row(p, x.s, x.b, key_of(n + 4));
+                    now = wanted(n) ? checked_row(D, next, key_of(n)) : -1;
+                    if (wanted(n + 4)) next = raw_row(D, x.s, x.b, key_of(n + 4));
                 }
                 const bool mine = (lane >> 3) == (n & 3) && now >= 0;
                 const int bytes = __popc(__ballot_sync(~0u, mine)) * D.box * RB;
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             ok = mbar_wait(&bars[T_MEET], meets++ & 1, &aborted, kDecWaitNs) && ok;
             __syncwarp();
         };
-        SeqInfo s;                     // of the segment in hand
+        Lens s;                        // of the segment in hand
         int b = 0, hk = 0, n_tiles = 0;
         float l[H];
         auto token = [&](int r) { return token_of(D, g.tile * R + r); };
@@ -667,7 +667,7 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     const bool wide = D.hc * C::RB >= 256 || D.p.Hkv == 1;
     D.box = D.p.paged && D.p.page_size < kTileKeys ? D.p.page_size : kTileKeys;
     if (!make_row_maps(D.p, D.k, D.v, D.box, wide, &maps.k, &maps.v)) return cudaErrorInvalidValue;
-    return launch_early(decode_tiles_kernel<FP8>, dim3(C::CTAS), C::THREADS, C::SMEM, s, D, maps);
+    return launch_early(decode_tiles_kernel<FP8>, dim3(D.hc, C::CTAS / D.hc), C::THREADS, C::SMEM, s, D, maps);
 }
 
 }  // namespace

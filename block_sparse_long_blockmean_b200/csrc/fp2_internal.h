@@ -120,7 +120,7 @@ struct DecodeParams {
     // set by the launchers: KV heads of an item, those of one CTA of it, groups of
     // heads, row tiles of the longest sequence, records by item (few) or by share
     int hc, hw, groups, tiles_max, few;
-    int g_shift;               // log2 of the query heads of a KV head
+    int g_shift, page_shift;   // log2 of the query heads of a KV head, of page_size
     int box;                   // rows of a copy of the tile kernel
 };
 constexpr int kDecHeads = 2;   // most KV heads of a CTA

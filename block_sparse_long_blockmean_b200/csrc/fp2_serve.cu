@@ -297,6 +297,7 @@ fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
     D.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
     D.record = reinterpret_cast<int4*>(ws + L.record);
     D.g_shift = __builtin_ctz((unsigned)kp.G);
+    D.page_shift = page_table ? __builtin_ctz((unsigned)kp.page_size) : 0;
     D.qk_scale = 1.4426950408889634f / std::sqrt((float)kp.d);
     return cuda_status(fp2::launch_decode(D, stream_of(P)));
 }
