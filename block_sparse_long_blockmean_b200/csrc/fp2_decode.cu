@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 }
             }
         };
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
 
         // ---- this warp's query columns, running (m, l, o) ----
@@ -614,8 +614,9 @@ __device__ __forceinline__ void finish_row(const DecodeParams& D, const Item& it
 constexpr int kJoinWarps = 16;
 
 // Few items, each of many parts: grid (items, hc * packed rows), a CTA per row,
-// whose warps add up every kJoinWarps-th part.  5.6 us for 4 items of 111 parts, most
-// of them its launch and two loads that wait for one another.
+// whose warps add up every kJoinWarps-th part.  About 5 us, most of them its launch, two
+// loads that wait for one another and code that is fetched as it runs: batches of
+// 8 parts and unrolled sums over the warps took 0.7 us more.
 template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid_constant__ DecodeParams D) {
     constexpr int R = 8 * NT, E = DH / 32;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     if (*D.p.err == kErrTimeout) return;  // records may be missing
     if (item.parts() == 0 || r >= item.rows()) return;
     float M, L, O[E];
-    add_parts<DH, R, E, 8>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
+    add_parts<DH, R, E, 2>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
 #pragma unroll
     for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = O[e];
     if (lane == 0) {
@@ -641,9 +642,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     M = -FLT_MAX;
     L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, sm_m[w]);
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < kJoinWarps; ++w) {
         const float f = ex2(sm_m[w] - M);
         L += f * sm_l[w];
