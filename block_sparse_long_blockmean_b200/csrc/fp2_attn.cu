@@ -36,7 +36,6 @@
 //               layout, and at the end normalises O and stores bf16 rows.
 // TMEM: S0 cols [0,128), S1 [128,256), O [256,256+d).
 #include "fp2_attn_common.cuh"
-#include "fp2_launch.cuh"
 
 namespace fp2 {
 
@@ -485,29 +484,15 @@ static EncodeTiledFn get_encode() {
 }
 
 static bool encode(CUtensorMap* m, bool fp8, int rank, const void* base, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box,
-                   CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+                   const cuuint64_t* strides, const cuuint32_t* box) {
     EncodeTiledFn fn = get_encode();
     if (!fn) return false;
     cuuint32_t es[4] = {1, 1, 1, 1};
     CUresult r = fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                     (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
-}
-
-bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, bool wide,
-                   CUtensorMap* mk, CUtensorMap* mv) {
-    const bool fp8 = p.fp8 != 0;
-    const cuuint64_t row = (cuuint64_t)p.d * (fp8 ? 1 : 2);
-    cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hkv,
-                          p.paged ? (cuuint64_t)p.num_pages * p.page_size : (cuuint64_t)p.total_k};
-    cuuint64_t str[2] = {row, p.Hkv * row};
-    cuuint32_t box[3] = {fp8 ? 128u : 64u, 1, (cuuint32_t)rows};
-    const CUtensorMapL2promotion l2 =
-        wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-    return encode(mk, fp8, 3, k, dims, str, box, l2) && encode(mv, fp8, 3, v, dims, str, box, l2);
 }
 
 bool make_attn_maps(const KParams& p, const void* q, const void* k, const void* v, int D,

@@ -8,11 +8,11 @@
 // + l2 2^(m2-m), o likewise; out = o / l, lse = ln 2 (m + log2 l).
 //
 // Split: the unit of work is 16 keys of one (sequence, group of hc adjacent KV
-// heads, row tile).  All units, in that order, are cut into equal shares, one
-// per CTA, so lengths may differ at will; every CTA finds its own share from the
-// lengths.  An item (sequence, head group, tile) that lies in one share is
-// finished there; one that spans several leaves a partial (m, l, o) per share in
-// the workspace and a join kernel reduces them.
+// heads, row tile).  All units, in that order, are cut into equal shares, so lengths
+// may differ at will; every CTA finds its own share from the lengths.  A share is
+// taken by hc / hw CTAs side by side, hw heads each.  An item (sequence, head group,
+// tile) that lies in one share is finished there; one that spans several leaves a
+// partial (m, l, o) per share in the workspace and a join kernel reduces them.
 //
 // Products: both on the tensor core with the keys (or the head dimension) as
 // the 16 rows of an m16n8 product and 8 packed query rows as its columns:
@@ -22,10 +22,10 @@
 // same two rows of S^T and O^T: the softmax's scaling never crosses lanes.
 //
 // Bound by the cache's bytes, each read once.  One sequence of 131072 bf16 keys, 32
-// heads over 8 (537 MB): 89 us, 6.0 TB/s; 128 ragged ones to 8191 keys (2.13 GB): 334
-// us, 6.4 TB/s; 8 e4m3 ones of 4K to 64K (486 MB): 89 us, 5.5 TB/s; 8 ragged bf16
-// ones to 4097 (73 MB): 24 us, of which 4 pass before the first keys are there and 5
-// in the join; one of 1024: 7.3 us, the two launches.  Loads alone reach 6.55 TB/s in
+// heads over 8 (537 MB): 87 us, 6.2 TB/s; 128 ragged ones to 8191 keys (2.13 GB): 315
+// us, 6.7 TB/s; 8 e4m3 ones of 4K to 64K (486 MB): 86 us, 5.7 TB/s; 8 ragged bf16
+// ones to 4097 (73 MB): 22 us, of which 4 pass before the first keys are there and 5
+// in the join; one of 1024: 6.8 us, the two launches.  Loads alone reach 6.55 TB/s in
 // pieces of 256 bytes and 5.7 in pieces of 128.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -676,13 +676,16 @@ template <int DH, bool FP8, int NT>
 cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using V = Variant<DH, FP8, NT>;
     // more than 16 packed rows at head dimension 128: tiles on the 5th-generation tensor
-    // core (4 tokens x 8 heads on 2 x 131072 e4m3 keys: 102 us, here 169; but 16 rows
-    // on 32768 bf16 keys: 65 us, here 53, and more so below)
+    // core (4 tokens x 8 heads on 262144 e4m3 keys: 102 us, here 169); up to 16 rows here
+    // (2 x 8 on 4 x 32768: e4m3 39 us, as tiles 44, bf16 55 and 57)
     constexpr bool TILES = DH == 128 && NT == 4;
     // (at least one: lengths above a limit of 0 have to be recorded)
     const int packed = D.p.max_seqlen_q > 0 ? D.p.max_seqlen_q * D.p.G : 1;
-    // KV heads of an item: those whose rows of a token are 1 KB together, two of them in
-    // a CTA where warps take its products, the others in the CTAs beside it
+    // KV heads of an item: those whose rows of a token are 2 KB together, two of them in
+    // a CTA where warps take its products, the others in the CTAs beside it, so that
+    // the DRAM reads a token's heads at about the same time (128 ragged bf16 sequences:
+    // 319 us, with 1 KB 323, with 512 bytes 332; 4 tokens on 4 x 32768 e4m3 keys: 47,
+    // with 512 bytes 55)
     D.hw = TILES || D.p.Hkv % 2 ? 1 : 2;
     D.hc = kHeadBytes / V::RB;
     while (D.p.Hkv % D.hc || D.hc % D.hw) --D.hc;
@@ -690,7 +693,9 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     D.tiles_max = (packed + V::R - 1) / V::R;
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
     const int shares = (TILES ? decode_tile_ctas(FP8) : V::CTAS) / (D.hc / D.hw);
-    // join by item where they are long: their parts are shared out over 16 warps a row
+    // join by item where an item spans some shares: its parts are shared out over 16 warps
+    // a row (131072 keys: 88.7 us, by share 102.4); else by share, most of 2 or 3 parts
+    // (64 sequences of 1024: 50.4 us, by item 60.4)
     D.few = items * 4 <= shares && D.p.num_seqs <= kThreads;
     cudaError_t e;
     if constexpr (TILES) {

@@ -4,8 +4,8 @@
 
 #include <float.h>
 
+#include "fp2_device.cuh"
 #include "fp2_launch.cuh"
-#include "fp2_seq.cuh"
 
 namespace fp2 {
 
@@ -23,16 +23,27 @@ struct DecodeMaps {
     CUtensorMap k, v;  // [rows][Hkv][d], boxes of some rows x 128 bytes of one head
 };
 
-// A sequence's lengths, as far as they matter here.  (Code before the first copy counts:
-// it is fetched as it runs, at about 30 cycles an instruction.)
+// A sequence's lengths.  load_lens() checks them against the call's limits and records
+// the error if they are bad.  Offsets are compared as they are, and differences taken
+// without a sign: a signed one may be taken not to wrap, and the comparison dropped.
+// (Short, like all code before the first copy: it is fetched as it runs, at about
+// 30 cycles an instruction.)
 struct Lens {
-    int q0, Lq, Lk, k0, P;
+    int q0, Lq, Lk, k0, P;  // first query row, new tokens, keys, first key row, keys before the tokens
 };
 __device__ __forceinline__ bool load_lens(const DecodeParams& D, int b, Lens& s) {
-    SeqInfo x;
-    const bool ok = load_seq(D.p, b, x);
-    s = {x.q0, x.Lq, x.Lk, x.k0, x.P};
-    return ok;
+    const KParams& p = D.p;
+    const int q1 = p.cu_q[b + 1];
+    s.q0 = p.cu_q[b];
+    s.Lq = (int)((unsigned)q1 - (unsigned)s.q0);
+    s.Lk = p.seqlens_k ? p.seqlens_k[b] : s.Lq;
+    s.k0 = p.paged ? 0 : p.cu_k[b];
+    s.P = (int)((unsigned)s.Lk - (unsigned)s.Lq);
+    const bool lens_ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= p.total_q && s.Lq <= p.max_seqlen_q && s.Lk >= s.Lq && s.Lk <= p.max_seqlen_k;
+    const bool keys_ok = p.paged ? s.Lk <= (long long)p.max_pages * p.page_size : s.k0 >= 0 && s.Lk <= p.total_k - s.k0;
+    if (lens_ok && keys_ok) return true;
+    set_error(p.err, lens_ok ? kErrBounds : kErrInvalid, kDetSeqLen);
+    return false;
 }
 
 struct Shape {

@@ -28,11 +28,11 @@
 // one issues the products.  They meet in mbarriers only, so that the copies run on
 // into the next segment.
 //
-// Bound by the cache's bytes and, 11 us above them, by the softmax's instructions: 4
-// tokens x 8 heads on 2 x 131072 e4m3 keys with factors (537 MB) 102 us, 5.3 TB/s; the
-// copies and products alone, with no softmax, 93.  A run of seconds reaches the power
-// limit and 1.73 GHz: 116 us.  K and V in one ring: 133 us (a value's place stays
-// taken until its product, a key's only until its logits).
+// Bound by the cache's bytes and, some 8 us above them, by the softmax's instructions: 4
+// tokens x 8 heads on 262144 e4m3 keys with factors (537 MB) 102 us, 5.3 TB/s (the
+// copies and products alone, with no softmax, 93); 4 x 32768 bf16 keys 54 us.  A run of
+// seconds reaches the power limit and 1.73 GHz: 117 us.  K and V in one ring: 133 us (a
+// value's place stays taken until its product, a key's only until its logits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -53,7 +53,7 @@ struct Tile {
     static constexpr int STAGE = HALVES * HALF;           // a tile of K or of V
     // e4m3 tiles arrive faster than a warpgroup takes their softmax: two CTAs on each
     // SM (133 us; one, whose rows two warpgroups share, 141).  bf16 stages leave room for
-    // one CTA, and two warpgroups help it (4 x 32768 keys: 52 us, one warpgroup 68).
+    // one CTA, and two warpgroups help it (4 x 32768 keys: 58 us, one warpgroup 78).
     static constexpr int PER_SM = FP8 ? 2 : 1;
     static constexpr int WGS = FP8 ? 1 : 2;               // softmax warpgroups
     static constexpr int H = kTileRows / WGS;             // rows of one

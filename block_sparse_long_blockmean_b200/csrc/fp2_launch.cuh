@@ -8,7 +8,7 @@
 // successor's waiting CTAs would take the places of those that still have work, or
 // hold them while a call behind it is placed (64 sequences of 4096 e4m3 keys in
 // a row of decode calls: 97 us a call, with a trigger in the join kernel 133).
-// What is saved is the launch latency (smallest decode: 10.4 us to 8.4).
+// What is saved is the launch latency.
 #pragma once
 
 #include <cuda.h>
@@ -16,7 +16,7 @@
 
 #include <atomic>
 
-#include "fp2_internal.h"
+#include "fp2_serve.h"
 
 namespace fp2 {
 
@@ -53,7 +53,7 @@ inline cudaError_t allow_smem(void (*kernel)(P...), int smem, std::atomic<unsign
 
 // Tensor maps of the K and V caches as [rows][Hkv][d], whether paged or not, with
 // boxes of `rows` rows x 128 bytes of one head in the 128-byte swizzle; L2 fetches
-// them in pieces of 256 (wide) or 128 bytes (fp2_attn.cu).
+// them in pieces of 256 (wide) or 128 bytes (fp2_serve.cu).
 bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, bool wide, CUtensorMap* mk, CUtensorMap* mv);
 
 }  // namespace fp2

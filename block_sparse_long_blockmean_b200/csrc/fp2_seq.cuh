@@ -28,18 +28,15 @@ struct SeqInfo {
 // On a violation it records the error (once per grid, first writer wins) and
 // returns false; the caller then skips its work.
 __device__ __forceinline__ bool load_seq(const KParams& p, int b, SeqInfo& s) {
-    // (differences in unsigned arithmetic, offsets compared as they are: a signed
-    // difference may be taken not to wrap, and the comparison with it dropped)
-    const int q1 = p.cu_q[b + 1];
     s.q0 = p.cu_q[b];
-    s.Lq = (int)((unsigned)q1 - (unsigned)s.q0);
+    s.Lq = p.cu_q[b + 1] - s.q0;
     s.Lk = p.seqlens_k ? p.seqlens_k[b] : s.Lq;
     s.k0 = p.paged ? 0 : p.cu_k[b];
-    s.P = (int)((unsigned)s.Lk - (unsigned)s.Lq);
-    const bool lens_ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= p.total_q && s.Lq <= p.max_seqlen_q &&
-                         s.Lk >= s.Lq && s.Lk <= p.max_seqlen_k;
-    const bool keys_ok = !p.uses_kv ? true : p.paged ? s.Lk <= (long long)p.max_pages * p.page_size
-                                 : (s.k0 >= 0 && s.Lk <= p.total_k - s.k0);
+    s.P = s.Lk - s.Lq;
+    const bool lens_ok = s.Lq >= 0 && s.Lq <= p.max_seqlen_q && s.Lk <= p.max_seqlen_k &&
+                         s.P >= 0 && s.q0 >= 0 && s.q0 + s.Lq <= p.total_q;
+    const bool keys_ok = !p.uses_kv ? true : p.paged ? (s.Lk + p.page_size - 1) / p.page_size <= p.max_pages
+                                 : (s.k0 >= 0 && s.k0 + s.Lk <= p.total_k);
     if (!lens_ok || !keys_ok) {
         set_error(p.err, lens_ok ? kErrBounds : kErrInvalid, kDetSeqLen);
         return false;

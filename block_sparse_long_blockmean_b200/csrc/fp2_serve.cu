@@ -5,7 +5,7 @@
 #include <cstring>
 
 #include "fp2.h"
-#include "fp2_internal.h"
+#include "fp2_launch.cuh"
 
 namespace {
 
@@ -68,6 +68,34 @@ DecodeLayout decode_layout(const fp2_params* P) {
 }
 
 }  // namespace
+
+namespace fp2 {
+
+bool make_row_maps(const KParams& p, const void* k, const void* v, int rows, bool wide, CUtensorMap* mk, CUtensorMap* mv) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* at = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &at, cudaEnableDefault, &found) == cudaSuccess &&
+                        found == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Encode>(at) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t row = (cuuint64_t)p.d * (p.fp8 ? 1 : 2);
+    const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hkv,
+                                p.paged ? (cuuint64_t)p.num_pages * p.page_size : (cuuint64_t)p.total_k};
+    const cuuint64_t strides[2] = {row, p.Hkv * row};
+    const cuuint32_t box[3] = {p.fp8 ? 128u : 64u, 1, (cuuint32_t)rows}, steps[3] = {1, 1, 1};
+    auto map = [&](CUtensorMap* m, const void* base) {
+        return encode(m, p.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                      strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(mk, k) && map(mv, v);
+}
+
+}  // namespace fp2
 
 extern "C" {
 
