@@ -538,3 +538,46 @@ def test_offsets_that_wrap_are_refused():
         p.check()
     assert (e.value.status, e.value.detail) == (fp2.FP2_ERR_INVALID_ARG, 1)
     assert (p.out == 3).all()
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,n", [
+    ("bf16", 3, 3, 128, 1), ("bf16", 20, 5, 128, 1), ("fp8", 7, 7, 128, 2), ("fp8", 16, 16, 128, 1), ("bf16", 12, 12, 128, 1),
+    ("fp8", 24, 24, 128, 1), ("bf16", 17, 17, 128, 1), ("bf16", 24, 24, 64, 1), ("bf16", 20, 10, 64, 9), ("bf16", 40, 5, 128, 3),
+    ("fp8", 48, 6, 128, 4), ("fp8", 10, 5, 128, 9), ("bf16", 96, 12, 128, 3), ("fp8", 136, 17, 128, 3), ("fp8", 33, 33, 128, 1)])
+@pytest.mark.parametrize("lk", [[700, 33, 3000], [40] * 30 + [900]])
+def test_numbers_of_heads(dtype, Hq, Hkv, d, n, lk):
+    """Heads that do not divide the CTAs, or one another."""
+    c = Case([n] * len(lk), lk, Hq, Hkv, d, 16, dtype, seed=31)
+    p = c.plan()
+    p.run()
+    c.check(p)
+
+
+@pytest.mark.parametrize("n,dtype", [(1, "bf16"), (4, "fp8"), (4, "bf16")])
+def test_two_calls_at_once(n, dtype):
+    """Calls on two streams, each with its own workspace, while the other runs."""
+    cases = [Case([n] * 5, [4000 + 700 * i for i in range(5)], 16, 2, 128, 64, dtype, seed=32 + k) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    plans = [c.plan(stream=s.cuda_stream) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p in plans:
+            p.run()
+    torch.cuda.synchronize()
+    for c, p in zip(cases, plans):
+        c.check(p)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_same_inputs_same_bits(n):
+    """Shares and joins in a fixed order: a second call, alone or after others, gives the same bits."""
+    c = Case([n] * 6, [10, 5000, 1, 4, 900, 2500] if n == 1 else [10, 5000, 7, 4, 900, 2500], 16, 2, 128, 16, "fp8", seed=34)
+    p, other = c.plan(), Case([1], [3000], 16, 2, 128, 16, "bf16", seed=35).plan()
+    p.run()
+    out, lse = p.out.clone(), p.lse.clone()
+    for _ in range(5):
+        other.run()
+        p.out.zero_()
+        p.run()
+        assert torch.equal(p.out.view(torch.uint8), out.view(torch.uint8)) and torch.equal(p.lse, lse)
+    c.check(p)
