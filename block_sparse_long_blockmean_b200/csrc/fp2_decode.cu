@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     wait_previous();
 
     Share share;  // a share is at least one unit of each warp
-    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.y, kw, h0 == 0, share)) return;
+    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.y, 3 - hw, h0 == 0, share)) return;
     const Lens& s = share.s;
     Segment seg;
     while (next_segment<R, kUnit>(D, share, seg)) {

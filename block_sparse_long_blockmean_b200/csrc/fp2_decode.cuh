@@ -112,17 +112,19 @@ __device__ __forceinline__ long long block_prefix(long long x, long long& total,
 }
 
 // Share c of `shares` at most: units [u, u_end) of `total` cut into `parts` equal
-// shares, starting in sequence b, whose units start at seq_at and whose lengths
-// are s.  False (for the whole CTA) if the share is empty.  A share has at least
-// `least` units.  With `records` also clears those that nobody else will write.
+// shares, the first `more` of them with `each` + 1 units, the others with `each`;
+// starting in sequence b, whose units start at seq_at and whose lengths are s.
+// False (for the whole CTA) if the share is empty.  The shares have about 2^least
+// units or more.  With `records` also clears those that nobody else will write.
 struct Share {
-    long long total, u, u_end, seq_at;
-    int parts, b;
+    long long u, u_end, seq_at, each, more;
+    int b;
     Lens s;
-    __device__ __forceinline__ long long start(int i) const { return quotient(total * i, parts); }
-    // the last share that an item reaches whose last unit is `end`: the largest i
-    // with start(i) <= end, that is total i < (end + 1) parts
-    __device__ __forceinline__ int of_unit(long long end) const { return (int)quotient((end + 1) * parts - 1, total); }
+    // the share that holds unit x
+    __device__ __forceinline__ int of_unit(long long x) const {
+        const long long large = more * (each + 1);
+        return (int)(x < large ? quotient(x, each + 1) : more + quotient(x - large, each));
+    }
 };
 template <int R, int UNIT, int W>
 __device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int shares, int least, bool records, Share& x) {
@@ -152,12 +154,13 @@ __device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int sha
             for (int j = tiles; j < D.tiles_max; ++j)
                 D.record[2 * ((threadIdx.x * D.groups + i) * D.tiles_max + j)] = make_int4(0, 0, 0, 0);
     }
-    const long long want = (total + least - 1) / least;
-    x.total = total;
-    x.parts = (int)(want < shares ? (want > 0 ? want : 1) : shares);
-    if (c >= x.parts || total == 0) return false;
-    x.u = x.start(c);
-    x.u_end = x.start(c + 1);
+    const long long want = (total + (1 << least) - 1) >> least;
+    const int parts = (int)(want < shares ? want : shares);
+    if (c >= parts) return false;
+    x.each = quotient(total, parts);
+    x.more = total - x.each * parts;
+    x.u = c * x.each + (c < x.more ? c : x.more);
+    x.u_end = x.u + x.each + (c < x.more ? 1 : 0);
     for (int b0 = 0;;) {
         if (n > 0 && at <= x.u && x.u < at + n) {
             found.b = b0 + threadIdx.x;

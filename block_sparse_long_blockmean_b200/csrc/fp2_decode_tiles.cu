@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
     }
     wait_previous();
     Share x;
-    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.y, 1, hs == 0, x)) return;
+    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.y, 0, hs == 0, x)) return;
     if (warp == MMA_WARP) {
         tmem_alloc(&tmem_at, C::TMEM);
         tmem_relinquish();
