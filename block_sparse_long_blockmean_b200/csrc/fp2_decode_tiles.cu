@@ -9,15 +9,17 @@
 // logits and, at the end, one d of the outputs.
 //
 // The weights P need more than one 8-bit (or bf16) operand to keep their
-// precision.  e4m3 caches: w is rounded to fp16 (11 bits) and cut into three e5m2
-// terms, each what is left rounded to 3 bits.  e5m2 is fp16's upper half, so a term
-// is an addition and a mask, and the rest an exact subtraction: of a value in
-// [2^e, 2^(e+1)), a multiple of 2^(e-10), the first term leaves at most 2^(e-3), the
-// second 2^(e-7), which the third holds whole.  They sum to the fp16 value down to
-// 2^-16, that is 2^-31 of the row's largest.  (Four terms cut off instead of rounded:
-// 105 us where three take 102, and 122 against 116 in a long run at the power limit.)
-// bf16 caches: two bf16 terms.  The terms are columns of one product, so V is read
-// once; their accumulators are added when the segment ends.
+// precision.  e4m3 caches: w is rounded to fp16 (11 bits; as in fp2_decode.cu) and cut
+// into three e5m2 terms, each what is left rounded to 3 bits.  e5m2 is fp16's upper half,
+// so a term is an addition and a mask, and the rest an exact subtraction.  What is left is
+// multiplied by 16 before the next term, and that term's accumulators by 1/16 when the
+// segment ends: of a value in [2^e, 2^(e+1)) the rest is at most 2^(e-3), so 2^(e+1) after
+// it, no term overflows, and the least of the third is 2^-24, fp16's own.  The terms sum to
+// the fp16 value, whatever it is in 0 .. 2^15.  (Unscaled terms end at e5m2's least, 2^-16,
+// where a key 17 below the row's largest logit is lost, and with it a whole tail beside one
+// key, a sink, that lies so far above the rest: 4 drafts on 256K keys 102.4 us, scaled 104.8.)
+// bf16 caches: two bf16 terms.  The terms are columns of one product, so V is read once; their
+// accumulators are added when the segment ends.
 //
 // Keys that only some of the tile's tokens see (at most 15, the new ones) stay out
 // of the second product, where a weight of 0 would not keep a value that is not
@@ -29,7 +31,7 @@
 // into the next segment.
 //
 // Bound by the cache's bytes and, some 8 us above them, by the softmax's instructions: 4
-// tokens x 8 heads on 262144 e4m3 keys with factors (537 MB) 102 us, 5.3 TB/s (the
+// tokens x 8 heads on 262144 e4m3 keys with factors (537 MB) 105 us, 5.1 TB/s (the
 // copies and products alone, with no softmax, 93); 4 x 32768 bf16 keys 54 us.  A run of
 // seconds reaches the power limit and 1.73 GHz: 117 us.  K and V in one ring: 133 us (a
 // value's place stays taken until its product, a key's only until its logits).
@@ -43,6 +45,7 @@ namespace fp2 {
 namespace {
 
 constexpr int kTileKeys = 128, kTileRows = 32;
+constexpr float kTermScale = 16.f;  // between an e4m3 cache's terms of a weight
 
 template <bool FP8>
 struct Tile {
@@ -350,12 +353,14 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                 tc_fence_after();
                 float o[H];
                 tmem_load(tmem + lanes + C::O_COL + first, o);
+                float down = 1.f;
 #pragma unroll 1
                 for (int k = 1; k < C::TERMS; ++k) {
                     float y[H];
                     tmem_load(tmem + lanes + C::O_COL + k * R + first, y);
+                    down *= FP8 ? 1.f / kTermScale : 1.f;
 #pragma unroll
-                    for (int i = 0; i < H; ++i) o[i] += y[i];
+                    for (int i = 0; i < H; ++i) o[i] = fmaf(y[i], down, o[i]);
                 }
                 tc_fence_before();
                 // the weights' place in shared memory takes the rows: its last reader is done
@@ -590,7 +595,9 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
 #pragma unroll
                         for (int i = 0; i < H / 2; ++i) {
                             cut[i] = (left[i] + 0x00800080u) & 0xFF00FF00u;
-                            if (k + 1 < C::TERMS) asm("sub.f16x2 %0, %0, %1;" : "+r"(left[i]) : "r"(cut[i]));
+                            if (k + 1 < C::TERMS)  // (x 16, kTermScale)
+                                asm("{\n\t.reg .b32 r;\n\tsub.f16x2 r, %0, %1;\n\tmul.f16x2 %0, r, %2;\n\t}"
+                                    : "+r"(left[i]) : "r"(cut[i]), "r"(0x4C004C00u));
                         }
 #pragma unroll
                         for (int h = 0; h < H / 16; ++h) {

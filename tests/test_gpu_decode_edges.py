@@ -1,0 +1,70 @@
+"""fp2_decode where its arithmetic is at its edges: one key far above a long flat
+tail.  Inputs and bounds as in test_gpu_decode.py."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_decode import E4M3, Case
+
+pytestmark = pytest.mark.gpu
+
+
+def stored(c, x, name):
+    """Rows [.., heads, d] in the case's type, by the heads' scales."""
+    if c.dtype == "fp8":
+        return (x / c.scales[name][:, None]).clamp(-448, 448).to(E4M3)
+    return x.bfloat16()
+
+
+def put(c, name, rows, x):
+    """Values of some cache rows (before any block factor)."""
+    flat = getattr(c, name).view(-1, c.Hkv, c.d)
+    x = stored(c, x, name)
+    if c.dtype == "fp8":
+        flat.view(torch.uint8)[rows] = x.view(torch.uint8)
+    else:
+        flat[rows] = x
+
+
+def sink(lq, lk, gap, dtype, Hq, Hkv, factors, noise, seed):
+    """Key 0 of each sequence `gap` above all others, its value 0; the others' logits
+    within a few `noise` of 0, their values near 1: the output is what the tail adds."""
+    c = Case(lq, lk, Hq, Hkv, 128, 64, dtype, seed=seed, factors=factors)
+    g = torch.Generator("cuda").manual_seed(900 + seed)
+    u = torch.where(torch.rand((Hkv, 128), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    T = c.q.shape[0]
+    q = 2 * u.repeat_interleave(Hq // Hkv, 0)[None] + 0.1 * torch.randn((T, Hq, 128), generator=g, device="cuda")
+    c.q.view(torch.uint8).copy_(stored(c, q, "q").view(torch.uint8))
+    for b, rows in enumerate(c.rows):
+        shape = (len(rows), Hkv, 128)
+        k, v = noise * torch.randn(shape, generator=g, device="cuda") / 2, 1 + 0.25 * torch.randn(shape, generator=g, device="cuda")
+        k[0] = gap / (2 * 128 ** 0.5) * u / (c.fac["k"][b, 0][:, None] if factors else 1.0)
+        v[0] = 0
+        put(c, "k", rows, k)
+        put(c, "v", rows, v)
+    return c
+
+
+@pytest.mark.parametrize("gap", [12.0, 15.0, 17.0])
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("dtype,factors", [("bf16", False), ("fp8", False), ("fp8", True)])
+def test_tail_under_a_sink(dtype, factors, n, gap):
+    """A long tail is not lost beside one key of nearly all the weight, whatever rounds
+    the weights, in one sequence over all CTAs ..."""
+    c = sink([n], [40000], gap, dtype, 8, 1, factors, 0.02, seed=40)
+    p = c.plan()
+    p.run()
+    c.check(p)
+
+
+@pytest.mark.parametrize("gap,noise", [(12.0, 0.0), (15.0, 0.0), (17.0, 0.5)])
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("dtype,factors", [("bf16", False), ("fp8", False), ("fp8", True)])
+def test_tails_under_sinks_of_whole_sequences(dtype, factors, n, gap, noise):
+    """... and in a batch whose sequences lie in one CTA's share each, with the sink."""
+    lk = (np.arange(40) * 7 + 2900).tolist()
+    c = sink([n] * 40, lk, gap, dtype, 64, 8, factors, noise, seed=41)
+    p = c.plan()
+    p.run()
+    # (a third of the sequences are compared: the 64-bit form walks them row by row)
+    c.check(p, skip=[b for b in range(40) if b % 3])
