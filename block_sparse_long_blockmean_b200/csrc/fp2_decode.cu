@@ -369,12 +369,15 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                     for (int e = 0; e < 2; ++e) {
                         const float f = FP8 ? sc[nt][e] * fac.x : sc[nt][e];
                         float y = fmaxf(z[nt][e] * f, z[nt][e + 2] * f);
-                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
-                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+                        float least = y;  // of pairs of keys
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) {
+                            y = fmaxf(y, __shfl_xor_sync(~0u, y, o));
+                            if (FP8) least = fminf(least, __shfl_xor_sync(~0u, least, o));
+                        }
                         if (y + neg_m[nt][e] > kRoof) {
-                            const float shrink = ex2(kLift - y - neg_m[nt][e]);
-                            neg_m[nt][e] = kLift - y;
+                            const float lift = lift_of<FP8>(y, least), shrink = ex2(lift - y - neg_m[nt][e]);
+                            neg_m[nt][e] = lift - y;
                             l[nt][e] *= shrink;
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {

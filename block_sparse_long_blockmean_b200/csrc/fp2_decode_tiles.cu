@@ -523,10 +523,12 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     softmax_sync(wg);
                     if (tid < H) {
                         const float most = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
+                        const float least = fminf(fminf(red[0][tid], red[1][tid]), fminf(red[2][tid], red[3][tid]));
+                        const float lift = lift_of<FP8>(most, least);
                         const float old = sm_nm[first + tid];
                         const bool moves = most + old > kRoof;
-                        sm_f[first + tid] = moves ? ex2(kLift - most - old) : 1.f;
-                        if (moves) sm_nm[first + tid] = kLift - most;
+                        sm_f[first + tid] = moves ? ex2(lift - most - old) : 1.f;
+                        if (moves) sm_nm[first + tid] = lift - most;
                     }
                     softmax_sync(wg);
 #pragma unroll

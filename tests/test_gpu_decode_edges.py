@@ -68,3 +68,16 @@ def test_tails_under_sinks_of_whole_sequences(dtype, factors, n, gap, noise):
     p.run()
     # (a third of the sequences are compared: the 64-bit form walks them row by row)
     c.check(p, skip=[b for b in range(40) if b % 3])
+
+
+@pytest.mark.parametrize("noise", [0.0, 0.02])
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("dtype,factors", [("bf16", False), ("fp8", False), ("fp8", True)])
+def test_tails_far_under_sinks(dtype, factors, n, noise):
+    """18 below the largest logit fp16 weights keep their 11 bits where the largest stands alone."""
+    lk = (np.arange(40) * 7 + 2900).tolist()
+    for lens in (lk, [40000]):
+        c = sink([n] * len(lens), lens, 18.0, dtype, 64, 8, factors, noise, seed=42)
+        p = c.plan()
+        p.run()
+        c.check(p, skip=[b for b in range(40) if b % 3])
