@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
             }
             if (whole) {
                 const int tok = token_of(D, tile * R + r), hkv = group * D.hc + h0 + hx, h = hkv * p.G + head_of(D, tile * R + r);
-                put_out(D, s.q0 + tok, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
+                put_out<FP8>(D, s.q0 + tok, h, col, O, L);
                 if (D.lse && col == 0) D.lse[(long long)(s.q0 + tok) * p.Hq + h] = lse_of(M, L);
             } else {
                 const size_t at = ((size_t)slot * D.hc + h0 + hx) * R + r;
@@ -610,7 +610,7 @@ template <bool FP8, int R>
 __device__ __forceinline__ void finish_row(const DecodeParams& D, const Item& item, int hx, int r, int col, float4 O, float M, float L) {
     const KParams& p = D.p;
     const int hkv = item.a.z * D.hc + hx, t = token_of(D, item.a.w * R + r), h = hkv * p.G + head_of(D, item.a.w * R + r);
-    put_out(D, item.a.y + t, h, col, scaled(O, (FP8 ? p.v_scale[hkv] : 1.f) / L));
+    put_out<FP8>(D, item.a.y + t, h, col, O, L);
     if (D.lse && col == 0) D.lse[(long long)(item.a.y + t) * p.Hq + h] = lse_of(M, L);
 }
 

@@ -238,24 +238,30 @@ __device__ __forceinline__ void put_record(const DecodeParams& D, const Share& x
     D.record[at + 1] = make_int4(g.rows, c, 0, 0);
 }
 
-// Four columns of one packed row's output, rounded once.
-__device__ __forceinline__ void put_out(const DecodeParams& D, long long row, int h, int col, float4 x) {
-    const KParams& p = D.p;
-    const long long at = (row * p.Hq + h) * p.d + col;
-    if (p.out_fp8) {
-        const float sc = p.out_scale ? p.out_scale[h] : p.v_scale[h >> D.g_shift];
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D.out) + at) = pack_e4m3x4(x.x / sc, x.y / sc, x.z / sc, x.w / sc);
-    } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(D.out) + at) =
-            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-    }
-}
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
 __device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
 __device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b f
     return make_float4(fmaf(b.x, f, a.x), fmaf(b.y, f, a.y), fmaf(b.z, f, a.z), fmaf(b.w, f, a.w));
 }
 
+// Four columns of one packed row's output, o / l, rounded once.  e4m3 without scales of
+// its own holds the stored values' units, as o does: the value scale, which may be 0,
+// stays out.
+template <bool FP8>
+__device__ __forceinline__ void put_out(const DecodeParams& D, long long row, int h, int col, float4 o, float l) {
+    const KParams& p = D.p;
+    const long long at = (row * p.Hq + h) * p.d + col;
+    const bool stored = p.out_fp8 && !p.out_scale;
+    float4 x = scaled(o, (FP8 && !stored ? p.v_scale[h >> D.g_shift] : 1.f) / l);
+    if (p.out_fp8) {
+        const float sc = stored ? 1.f : p.out_scale[h];
+        x = sc == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x / sc, x.y / sc, x.z / sc, x.w / sc);
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D.out) + at) = pack_e4m3x4(x.x, x.y, x.z, x.w);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(D.out) + at) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
+}
 // Multi-token tiles of head dimension 128 (fp2_decode_tiles.cu): the shares'
 // partial rows and records, as decode_kernel leaves them for 32 rows a tile.
 cudaError_t launch_decode_tiles(const DecodeParams& D, cudaStream_t s);

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                         O = plus(O, V, sm_w[k][r]);
                     }
                     if (g.whole()) {
-                        put_out(D, s.q0 + token(r), head(r), col, scaled(O, (FP8 ? p.v_scale[hk] : 1.f) / sm_l[r]));
+                        put_out<FP8>(D, s.q0 + token(r), head(r), col, O, sm_l[r]);
                         if (D.lse && col == 0) D.lse[(long long)(s.q0 + token(r)) * p.Hq + head(r)] = lse_of(sm_m[r], sm_l[r]);
                     } else {
                         const size_t at = ((size_t)slot * D.hc + hs) * R + r;

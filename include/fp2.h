@@ -395,8 +395,8 @@ size_t fp2_decode_workspace_size(const fp2_params* params);
  * CTA, whatever the lengths (they are read on the device, so a captured graph
  * follows them); a head whose keys lie in several shares is joined by a second
  * kernel.  Arguments, supported shapes and dtypes as fp2_attn (block matters
- * for k_block_factor and the page size only); out as fp2_prefill's, rows behind
- * the last sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys
+ * for k_block_factor and the page size only); out as fp2_prefill's (an out_scale
+ * of 0 stores zeros), rows behind the last sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys
  * may hold anything, NaN included.  out and lse must not overlap the inputs or
  * each other.  group_masks, attn_kernel and the debug
  * fields have no effect.  The workspace's contents need not survive between

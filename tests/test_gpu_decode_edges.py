@@ -1,9 +1,10 @@
 """fp2_decode where its arithmetic is at its edges: one key far above a long flat
-tail.  Inputs and bounds as in test_gpu_decode.py."""
+tail, scales of 0.  Inputs and bounds as in test_gpu_decode.py."""
 import numpy as np
 import pytest
 import torch
 
+from block_sparse_long_blockmean_b200 import fp2
 from tests.test_gpu_decode import E4M3, Case
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +82,41 @@ def test_tails_far_under_sinks(dtype, factors, n, noise):
         p = c.plan()
         p.run()
         c.check(p, skip=[b for b in range(40) if b % 3])
+
+
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("lk", [[170, 40], [9000]])
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_a_scale_of_zero_with_e4m3_output(n, lk, which):
+    """A KV head (or query head) of zeros; without scales of its own the output is in the stored
+    values' units: for v_scale 0 it is finite, what the other scales' outputs would be for 1."""
+    c = Case([n] * len(lk), lk, 16, 2, 128, 16, "fp8", seed=43)
+    p = c.plan(out_dtype=fp2.FP2_FP8_E4M3)
+    p.run()
+    c.check(p, out_scale=c.scales["v"].repeat_interleave(8))
+    first = p.out.view(torch.uint8).clone()
+    c.scales[which][0] = 0.0
+    p.out.view(torch.uint8).fill_(0x7F)
+    p.run()
+    if which == "v":
+        p.check()
+        assert torch.equal(p.out.view(torch.uint8), first)
+    else:
+        c.check(p, out_scale=c.scales["v"].repeat_interleave(8))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("n", [1, 4])
+def test_an_output_scale_of_zero(dtype, n):
+    """An output scale of 0 stores zeros (and the other heads as they are)."""
+    c = Case([n, n], [170, 40], 8, 1, 128, 16, dtype, seed=44)
+    sc = torch.linspace(0.002, 0.02, 8, device="cuda")
+    p = c.plan(out_dtype=fp2.FP2_FP8_E4M3, out_scale=sc)
+    p.run()
+    c.check(p, out_scale=sc)
+    first = p.out.view(torch.uint8).clone()
+    sc[3] = 0.0
+    p.run()
+    p.check()
+    first[:, 3] = 0
+    assert torch.equal(p.out.view(torch.uint8), first)
