@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kAppThreads, 6) append_kernel(const __grid_con
                 if (on(i)) raw = mine[i * kAppThreads];
                 Quad a = unpack(make_uint2(raw.x, raw.y)), b = unpack(make_uint2(raw.z, raw.w));
                 // (the reciprocal is off by 2^-23 of its value, far below e4m3's 2^-4)
-                float r = FP8 ? __fdividef(1.f, inv[i]) : 1.f;
+                // a scale of 0 stands for a head of zeros, here as in fp2_decode
+                float r = !FP8 ? 1.f : inv[i] == 0.f ? 0.f : __fdividef(1.f, inv[i]);
                 if constexpr (TURN) {
                     if (norm) {
                         float2 q = ffma2(a.y, a.y, mul2(a.x, a.x));

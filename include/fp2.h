@@ -370,7 +370,8 @@ typedef struct fp2_append_io {
  *   (a, b) = rope_scale * (a cos - b sin, b cos + a sin), the angle being
  *            position * inv_freq[i], taken without rounding it  (q, k)
  * in fp32, rounded once: to bf16, or (FP2_FP8_E4M3) to e4m3 of x / scale with
- * params->q_scale, k_scale, v_scale, saturating.  v is only stored.  A slot
+ * params->q_scale, k_scale, v_scale, saturating (a scale of 0 stands for a head
+ * of zeros and stores zeros).  v is only stored.  A slot
  * outside the cache other than a negative one records FP2_ERR_DEVICE_BOUNDS
  * (detail 7) and is not written.  Slots other than -1 have to differ: of two
  * tokens with one slot, the row ends up with parts of either.
