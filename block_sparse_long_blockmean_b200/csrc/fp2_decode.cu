@@ -274,8 +274,6 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 const int r = min(nt * 8 + 2 * t4 + e, rows - 1);
                 last[nt][e] = s.P + token_of(D, tile * R + r);
                 sc[nt][e] = D.qk_scale * (FP8 ? q_scale[nt][e] * k_scale : 1.f);
-                // (a scale of 0 stands for a head of zeros; a masked logit stays -inf)
-                if (FP8 && sc[nt][e] == 0.f) sc[nt][e] = 1e-30f;
                 neg_m[nt][e] = FLT_MAX;
                 l[nt][e] = 0.f;
             }
@@ -340,13 +338,14 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                         *reinterpret_cast<uint4*>(my_ring + stage * V::STAGE + V::STAGE / 2 + h * V::TILE + y * 16) = make_uint4(0u, 0u, 0u, 0u);
                 __syncwarp();
             };
-            if (j0 + kUnit > seen_all) {
+            auto mask = [&](float (&x)[NT][4]) {  // keys that a row does not see
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (j0 + g + (e >> 1) * 8 > last[nt][e & 1]) z[nt][e] = -INFINITY;
-            }
+                        if (j0 + g + (e >> 1) * 8 > last[nt][e & 1]) x[nt][e] = -INFINITY;
+            };
+            if (j0 + kUnit > seen_all) mask(z);
             // exponents of the weights; m moves when one passes the roof
             float w[NT][4], top = -FLT_MAX;
 #pragma unroll
@@ -389,6 +388,9 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                         w[nt][e + 2] = fmaf(z[nt][e + 2], f, neg_m[nt][e]);
                     }
             }
+            // (again: a scale of 0, which stands for a head of zeros, or one whose product
+            // with a factor is 0 has made NaN of -inf; the maxima above pass over it)
+            if (FP8 && j0 + kUnit > seen_all) mask(w);
             {
                 // weights as the 16-bit operand: fp16 (11 bits) beside e4m3 values;
                 // beside bf16 ones two bf16 terms (16 bits), so that the weights'

@@ -120,3 +120,16 @@ def test_an_output_scale_of_zero(dtype, n):
     p.check()
     first[:, 3] = 0
     assert torch.equal(p.out.view(torch.uint8), first)
+
+
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("scale,factor", [(0.0, 1e-30), (0.0, 1.0), (1e-25, 1e-25)])
+def test_logits_scales_whose_product_is_zero(n, scale, factor):
+    """Every logit 0, whatever way the product of the scales becomes 0: the output is the mean of
+    the values seen, and masked keys are not among them."""
+    c = Case([n, n], [165, 37], 8, 1, 128, 16, "fp8", seed=45, factors=True)
+    c.scales["k"][0] = scale
+    c.fac["k"].fill_(factor)
+    p = c.plan()
+    p.run()
+    c.check(p)
