@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;  // (4: a CTA of hw = 1, 2 heads has 1 << (3 - hw) warps a head)
 constexpr int kUnit = kDecBox;  // keys of a unit: one copy
+constexpr int kWithheld = -2;   // instead of a row: a copy that does not come (tests of the waits' limit)
 constexpr int kHeadBytes = 2048;  // of the heads' rows of a token that are read together
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
@@ -158,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
     uint32_t phases = 0;  // parity of each stage's next completion
     wait_previous();
 
+    __shared__ Share found;
     Share share;  // a share is at least one unit of each warp
-    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.y, 3 - hw, h0 == 0, share)) return;
+    if (!find_share<R, kUnit, kWarps>(D, c, gridDim.y, 3 - hw, h0 == 0, found, share)) return;
     const Lens& s = share.s;
     Segment seg;
     while (next_segment<R, kUnit>(D, share, seg)) {
@@ -187,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
         };
         auto begin_round = [&](int n0) {
             row_now = n0 + lane < steps ? checked_row(D, raw_next, key_at(n0 + lane)) : -1;
+            if (n0 + lane + 1 == p.withhold_k_item) row_now = kWithheld;
             fac_now = fac_next;
             if (FP8 && p.kb_fac && !(fac_now.x > 0.f && fac_now.x <= 1.f && fac_now.y > 0.f && fac_now.y <= 1.f)) {
                 set_error(p.err, kErrInvalid, kDetFactor);
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 uint64_t* bar = &full[warp][stage];
                 const uint32_t dst = my_smem + stage * V::STAGE;
                 if (row0 < 0) {  // a page id out of range, recorded: nothing is read
-                    mbar_arrive(bar);
+                    if (row0 != kWithheld) mbar_arrive(bar);
                 } else {
                     mbar_arrive_expect_tx(bar, V::STAGE);
 #pragma unroll
@@ -291,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
 
         int stage = 0, fill = STAGES - 1;
         for (int i = 0; i < steps; ++i) {
-            if (!mbar_wait(&full[warp][stage], (phases >> stage) & 1, &aborted, kDecWaitNs)) break;
+            // (the warp's lanes go on or give up together)
+            if (!__all_sync(~0u, mbar_wait(&full[warp][stage], (phases >> stage) & 1, &aborted, p.wait_limit_ns))) break;
             phases ^= 1u << stage;
             __syncwarp();
             issue(i + STAGES - 1, fill);
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
             if (lane == 0) set_error(p.err, kErrTimeout, kDetWaitBase);
             for (int i = 0; i < STAGES; ++i) {
                 int ignore = 0;
-                mbar_wait(&full[warp][i], (phases >> i) & 1, &ignore, kDecWaitNs / 100);
+                mbar_wait(&full[warp][i], (phases >> i) & 1, &ignore, kDrainNs);
             }
         }
         __syncwarp();
@@ -514,7 +518,10 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 }
             }
         __syncthreads();
-        if (aborted) return;
+        if (aborted) {
+            if (threadIdx.x == 0 && h0 == 0) drop_records<R, kUnit>(D, found, share, c);
+            return;
+        }
         const bool whole = seg.whole();
         const int slot = 2 * c + (x0 == 0 ? 1 : 0);
         for (int y = threadIdx.x; y < hw * rows * (DH / 4); y += kThreads) {
@@ -631,7 +638,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hx = blockIdx.y % D.hc, r = blockIdx.y / D.hc;
     const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
-    if (*D.p.err == kErrTimeout) return;  // records may be missing
     if (item.parts() == 0 || r >= item.rows()) return;
     float M, L, O[E];
     add_parts<DH, R, E, 2>(D, item, hx, r, warp, kJoinWarps, lane, M, L, O);
@@ -667,7 +673,6 @@ __global__ void __launch_bounds__(32 * kShareWarps) join_shares_kernel(const __g
     wait_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hx = blockIdx.y;
     const Item item{D.record[2 * blockIdx.x], D.record[2 * blockIdx.x + 1]};
-    if (*D.p.err == kErrTimeout) return;  // records may be missing
     if (item.parts() == 0) return;
     for (int r = warp; r < item.rows(); r += kShareWarps) {
         float M, L, O[4];

@@ -9,7 +9,7 @@
 
 namespace fp2 {
 
-constexpr uint64_t kDecWaitNs = 2000000000ull;  // 2 s per wait for a copy or a product
+constexpr uint64_t kDrainNs = 20000000ull;      // 20 ms per copy in flight after a wait has run out
 constexpr int kFactorKeys = 128;                // keys that share their scale factors (e4m3's only block)
 constexpr int kDecBox = 16;                     // rows of a copy: they never cross a page
 
@@ -123,11 +123,13 @@ __device__ __forceinline__ long long block_prefix(long long x, long long& total,
 
 // Share c of `shares` at most: units [u, u_end) of `total` cut into `parts` equal
 // shares, the first `more` of them with `each` + 1 units, the others with `each`;
-// starting in sequence b, whose units start at seq_at and whose lengths are s.
-// False (for the whole CTA) if the share is empty.  The shares have about 2^least
-// units or more.  With `records` also clears those that nobody else will write.
+// starting in sequence b, whose units start at seq_at and whose lengths are s (`found`, in
+// shared memory, keeps these three).  False (for the whole CTA) if the share is empty.  The
+// shares have about 2^least units or more.  With `records` also clears those that nobody
+// else will write.
 struct Share {
     long long u, u_end, seq_at, each, more;
+    __device__ __forceinline__ long long start(int c) const { return c * each + (c < more ? c : more); }
     int b;
     Lens s;
     // the share that holds unit x
@@ -137,9 +139,8 @@ struct Share {
     }
 };
 template <int R, int UNIT, int W>
-__device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int shares, int least, bool records, Share& x) {
+__device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int shares, int least, bool records, Share& found, Share& x) {
     __shared__ long long sums[W];
-    __shared__ Share found;
     __shared__ long long chunk_end;
     const KParams& p = D.p;
     constexpr int T = 32 * W;
@@ -169,7 +170,7 @@ __device__ __forceinline__ bool find_share(const DecodeParams& D, int c, int sha
     if (c >= parts) return false;
     x.each = quotient(total, parts);
     x.more = total - x.each * parts;
-    x.u = c * x.each + (c < x.more ? c : x.more);
+    x.u = x.start(c);
     x.u_end = x.u + x.each + (c < x.more ? 1 : 0);
     for (int b0 = 0;;) {
         if (n > 0 && at <= x.u && x.u < at + n) {
@@ -242,6 +243,24 @@ __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)
 __device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
 __device__ __forceinline__ float4 plus(float4 a, float4 b, float f) {  // a + b f
     return make_float4(fmaf(b.x, f, a.x), fmaf(b.y, f, a.y), fmaf(b.z, f, a.z), fmaf(b.w, f, a.w));
+}
+
+// One thread of a CTA that gave up a wait: nothing is to be joined of the items that start
+// in its share.  (By share: its one record was cleared at the start, and its last segment
+// alone writes it.)  Their records would else be an earlier call's, with rows and shares of
+// its own; the error word cannot tell the join, as it keeps the first error.
+template <int R, int UNIT>
+__device__ __forceinline__ void drop_records(const DecodeParams& D, const Share& found, Share x, int c) {
+    if (!D.few) return;
+    x.u = x.start(c);
+    x.b = found.b;
+    x.seq_at = found.seq_at;
+    x.s = found.s;
+    Segment g;
+    while (next_segment<R, UNIT>(D, x, g)) {
+        if (g.x0 == 0) D.record[2 * ((x.b * D.groups + g.group) * D.tiles_max + g.tile)] = make_int4(0, 0, 0, 0);
+        x.u = g.item_at + g.x1;
+    }
 }
 
 // Four columns of one packed row's output, o / l, rounded once.  e4m3 without scales of

@@ -161,8 +161,9 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
         prefetch_tmap(&maps.v);
     }
     wait_previous();
+    __shared__ Share found;
     Share x;
-    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.y, 0, hs == 0, x)) return;
+    if (!find_share<R, kTileKeys, C::WARPS>(D, c, gridDim.y, 0, hs == 0, found, x)) return;
     if (warp == MMA_WARP) {
         tmem_alloc(&tmem_at, C::TMEM);
         tmem_relinquish();
@@ -193,14 +194,15 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     now = wanted(n) ? checked_row(D, next, key_of(n)) : -1;
                     if (wanted(n + 4)) next = raw_row(D, x.s, x.b, key_of(n + 4));
                 }
-                const bool mine = (lane >> 3) == (n & 3) && now >= 0;
+                const bool withheld = n + 1 == p.withhold_k_item;  // (tests of the waits' limit)
+                const bool mine = (lane >> 3) == (n & 3) && now >= 0 && !withheld;
                 const int bytes = __popc(__ballot_sync(~0u, mine)) * D.box * RB;
                 // one of the tile's operands into its ring
                 auto copy = [&](const CUtensorMap* map, int stages, int offset, int full, int empty) {
                     const int st = t % stages;
-                    if (t >= stages && !__all_sync(~0u, mbar_wait(&bars[empty + st], (t / stages - 1) & 1, &aborted, kDecWaitNs)))
+                    if (t >= stages && !__all_sync(~0u, mbar_wait(&bars[empty + st], (t / stages - 1) & 1, &aborted, p.wait_limit_ns)))
                         return false;
-                    if (lane == 0) mbar_arrive_expect_tx(&bars[full + st], bytes);
+                    if (lane == 0 && !withheld) mbar_arrive_expect_tx(&bars[full + st], bytes);
                     __syncwarp();
                     if (mine) {
                         const uint32_t dst = base + offset + st * C::STAGE + (lane & 7) * D.box * 128;
@@ -225,9 +227,9 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
         // never leave with copies in flight
         int ignore = 0;
         for (int i = max(0, k_copies - C::K_STAGES); i < k_copies; ++i)
-            mbar_wait(&bars[T_K_FULL + i % C::K_STAGES], (i / C::K_STAGES) & 1, &ignore, kDecWaitNs);
+            mbar_wait(&bars[T_K_FULL + i % C::K_STAGES], (i / C::K_STAGES) & 1, &ignore, kDrainNs);
         for (int i = max(0, t - C::V_STAGES); i < t; ++i)
-            mbar_wait(&bars[T_V_FULL + i % C::V_STAGES], (i / C::V_STAGES) & 1, &ignore, kDecWaitNs);
+            mbar_wait(&bars[T_V_FULL + i % C::V_STAGES], (i / C::V_STAGES) & 1, &ignore, kDrainNs);
     } else if (warp == MMA_WARP) {
         // ---------------------------------------------------------- products ---
         if (lane == 0) {
@@ -243,12 +245,12 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             int k_stage = 0, k_phase = 0, v_stage = 0, v_phase = 0;
             for (int seg = 0; ok && next_segment<R, kTileKeys>(D, x, g); ++seg) {
                 const int n_tiles = g.x1 - g.x0;
-                ok = mbar_wait(&bars[T_Q_READY], seg & 1, &aborted, kDecWaitNs);
+                ok = mbar_wait(&bars[T_Q_READY], seg & 1, &aborted, p.wait_limit_ns);
                 for (int n = 0; ok && n <= n_tiles; ++n) {
                     if (n < n_tiles) {
                         const int i = t + n, buf = i & 1;
-                        ok = mbar_wait(&bars[T_K_FULL + k_stage], k_phase, &aborted, kDecWaitNs) &&
-                             (i < 2 || mbar_wait(&bars[T_S_FREE + buf], (i / 2 - 1) & 1, &aborted, kDecWaitNs));
+                        ok = mbar_wait(&bars[T_K_FULL + k_stage], k_phase, &aborted, p.wait_limit_ns) &&
+                             (i < 2 || mbar_wait(&bars[T_S_FREE + buf], (i / 2 - 1) & 1, &aborted, p.wait_limit_ns));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t at = dk + (uint32_t)(k_stage * (C::STAGE >> 4));
@@ -268,8 +270,8 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     }
                     if (n >= 1) {
                         const int i = t + n - 1;
-                        ok = mbar_wait(&bars[T_V_FULL + v_stage], v_phase, &aborted, kDecWaitNs) &&
-                             mbar_wait(&bars[T_P_READY + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs);
+                        ok = mbar_wait(&bars[T_V_FULL + v_stage], v_phase, &aborted, p.wait_limit_ns) &&
+                             mbar_wait(&bars[T_P_READY + (i & 1)], (i >> 1) & 1, &aborted, p.wait_limit_ns);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t at = dv + (uint32_t)(v_stage * (C::STAGE >> 4));
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             // every product is done before TMEM is given back
             mma_commit(&bars[T_DRAIN]);
             int ignore = 0;
-            mbar_wait(&bars[T_DRAIN], 0, &ignore, kDecWaitNs);
+            mbar_wait(&bars[T_DRAIN], 0, &ignore, 100 * kDrainNs);
         }
     } else {
         // ----------------------------------------------------------- softmax ---
@@ -309,12 +311,12 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
             if (lane == 0) mbar_arrive(bar);
         };
         // the product of tile i has read its weights and values
-        auto product_done = [&](int i) { return mbar_wait(&bars[T_O_DONE + (i & 1)], (i >> 1) & 1, &aborted, kDecWaitNs); };
+        auto product_done = [&](int i) { return mbar_wait(&bars[T_O_DONE + (i & 1)], (i >> 1) & 1, &aborted, p.wait_limit_ns); };
         bool ok = true, dead = false;  // this thread's waits; the warps' common verdict
         int meets = 0;                 // of the two warpgroups
         auto meet = [&] {
             arrive(&bars[T_MEET]);
-            ok = mbar_wait(&bars[T_MEET], meets++ & 1, &aborted, kDecWaitNs) && ok;
+            ok = mbar_wait(&bars[T_MEET], meets++ & 1, &aborted, p.wait_limit_ns) && ok;
             __syncwarp();
         };
         Lens s;                        // of the segment in hand
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     set_error(p.err, kErrInvalid, kDetFactor);
                     fac = make_float2(1.f, 1.f);
                 }
-                ok = mbar_wait(&bars[T_S_FULL + buf], (t >> 1) & 1, &aborted, kDecWaitNs) && ok;
+                ok = mbar_wait(&bars[T_S_FULL + buf], (t >> 1) & 1, &aborted, p.wait_limit_ns) && ok;
                 __syncwarp();
                 tc_fence_after();
                 const bool seen = j0 + tid < g.seen_all;
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
 #pragma unroll
                 for (int k = 0; k < CHUNKS; ++k) *reinterpret_cast<uint4*>(p_row + ((chunk[k] ^ (tid & 7)) << 4)) = out[k];
                 if (edge) {
-                    ok = mbar_wait(&bars[T_V_FULL + t % C::V_STAGES], (t / C::V_STAGES) & 1, &aborted, kDecWaitNs) && ok;
+                    ok = mbar_wait(&bars[T_V_FULL + t % C::V_STAGES], (t / C::V_STAGES) & 1, &aborted, p.wait_limit_ns) && ok;
                     __syncwarp();
                 }
                 if (edge && !seen) {
@@ -664,6 +666,7 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM);
     }
+    if (aborted && threadIdx.x == 0 && hs == 0) drop_records<R, kTileKeys>(D, found, x, c);
 }
 
 template <bool FP8>

@@ -46,7 +46,7 @@ bool overlap(const void* a, size_t n, const void* b, size_t m) {
 fp2_status check_decode(const fp2_params* P) {
     if (!P) return FP2_ERR_INVALID_ARG;
     if (P->num_seqs < 1 || P->max_seqlen_q < 0 || P->max_seqlen_k < P->max_seqlen_q ||
-        P->max_seqlen_k < 1)
+        P->max_seqlen_k < 1 || P->debug_withhold_k_item < 0)
         return FP2_ERR_INVALID_ARG;
     fp2_status st = check_heads(P);
     if (st != FP2_OK) return st;
@@ -304,6 +304,8 @@ fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
     kp.nkb_max = (int)(((long long)P->max_seqlen_k + block - 1) / block);
     kp.fp8 = fp8;
     kp.uses_kv = 1;
+    kp.wait_limit_ns = P->debug_wait_limit_us ? P->debug_wait_limit_us * 1000ull : 2000000000ull;
+    kp.withhold_k_item = P->debug_withhold_k_item;
     kp.out_fp8 = P->out_dtype == FP2_FP8_E4M3;
     kp.out_scale = P->out_scale;
     kp.kb_fac = P->k_block_factor;

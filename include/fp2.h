@@ -114,14 +114,15 @@ typedef struct fp2_params {
     int attn_kernel;           /* 0 (default): the two-tile attention kernel.  1: the one-tile
                                   kernel (same results within rounding; for tests) */
     unsigned int debug_wait_limit_us; /* 0 (default): every pipeline wait inside the
-                                  attention kernel gives up after 2 s, records
+                                  attention kernel (and fp2_decode) gives up after 2 s, records
                                   FP2_ERR_TIMEOUT and ends its CTA cleanly.  > 0: after this
                                   many microseconds instead (tests of that path) */
     int debug_withhold_k_item; /* 0 (default).  > 0, tests only: the two-tile kernel's
                                   producer never loads the K tile of that work item
                                   (1-based) in any CTA, so the consumer's bounded wait runs
                                   out and the call records FP2_ERR_TIMEOUT; the output is
-                                  then undefined.  Never set in normal use */
+                                  then undefined.  fp2_decode: K and V of that copy of every
+                                  warp's (or tile loop's) range.  Never set in normal use */
     const float* k_block_factor; /* e4m3 only, optional (NULL: one scale per head): a KV
                                   cache quantised per key block.  Device fp32
                                   [num_seqs][ceil(max_seqlen_k / block)][Hkv]: key block j of
@@ -399,12 +400,13 @@ size_t fp2_decode_workspace_size(const fp2_params* params);
  * for k_block_factor and the page size only); out as fp2_prefill's (an out_scale
  * of 0 stores zeros), rows behind the last sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys
  * may hold anything, NaN included.  out and lse must not overlap the inputs or
- * each other.  group_masks, attn_kernel and the debug
- * fields have no effect.  The workspace's contents need not survive between
+ * each other.  group_masks and attn_kernel have no effect.  The workspace's contents need not survive between
  * calls; calls that share one must be ordered on a stream.
  * max_seqlen_q above FP2_DECODE_MAX_Q: FP2_ERR_UNSUPPORTED (fp2_prefill takes
  * those).  Device-side errors as fp2_attn; a sequence with bad lengths or a
- * page id out of range has undefined out and lse rows. */
+ * page id out of range has undefined out and lse rows, after FP2_ERR_TIMEOUT all
+ * sequences have.  Nothing but the call's own rows is written in either case, and
+ * an error that was not read yet does not change the next call's results. */
 fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* page_table, const int32_t* cu_seqlens, int block,
                       fp2_dtype dtype, void* out, float* lse, const fp2_params* params);
