@@ -28,15 +28,17 @@ struct SeqInfo {
 // On a violation it records the error (once per grid, first writer wins) and
 // returns false; the caller then skips its work.
 __device__ __forceinline__ bool load_seq(const KParams& p, int b, SeqInfo& s) {
+    // (differences are taken without a sign and no sum is compared: a signed one that
+    // wraps would pass for a short length, or its comparison be dropped)
     s.q0 = p.cu_q[b];
-    s.Lq = p.cu_q[b + 1] - s.q0;
+    s.Lq = (int)((unsigned)p.cu_q[b + 1] - (unsigned)s.q0);
     s.Lk = p.seqlens_k ? p.seqlens_k[b] : s.Lq;
     s.k0 = p.paged ? 0 : p.cu_k[b];
-    s.P = s.Lk - s.Lq;
+    s.P = (int)((unsigned)s.Lk - (unsigned)s.Lq);
     const bool lens_ok = s.Lq >= 0 && s.Lq <= p.max_seqlen_q && s.Lk <= p.max_seqlen_k &&
-                         s.P >= 0 && s.q0 >= 0 && s.q0 + s.Lq <= p.total_q;
-    const bool keys_ok = !p.uses_kv ? true : p.paged ? (s.Lk + p.page_size - 1) / p.page_size <= p.max_pages
-                                 : (s.k0 >= 0 && s.k0 + s.Lk <= p.total_k);
+                         s.Lk >= s.Lq && s.q0 >= 0 && s.Lq <= p.total_q - s.q0;
+    const bool keys_ok = !p.uses_kv ? true : p.paged ? (s.Lk - 1) / p.page_size < p.max_pages
+                                 : (s.k0 >= 0 && s.Lk <= p.total_k - s.k0);
     if (!lens_ok || !keys_ok) {
         set_error(p.err, lens_ok ? kErrBounds : kErrInvalid, kDetSeqLen);
         return false;
