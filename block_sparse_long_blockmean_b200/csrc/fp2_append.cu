@@ -258,7 +258,7 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
     if (p.d == 128) return p.fp8 ? launch<128, true>(p, s) : launch<128, false>(p, s);
-    return p.fp8 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+    return launch<64, false>(p, s);  // (e4m3 is head dimension 128 only)
 }
 
 }  // namespace fp2

@@ -162,6 +162,7 @@ fp2_status fp2_append(const fp2_append_io* io, fp2_dtype dtype, const fp2_params
     if (dtype != FP2_BF16 && dtype != FP2_FP8_E4M3) return FP2_ERR_INVALID_ARG;
     const bool fp8 = dtype == FP2_FP8_E4M3;
     if (P->k_block_factor || P->v_block_factor) return FP2_ERR_UNSUPPORTED;
+    if (fp8 && P->head_dim != 128) return FP2_ERR_UNSUPPORTED;
     if (fp8 && (!P->q_scale || !P->k_scale || !P->v_scale)) return FP2_ERR_INVALID_ARG;
     if (P->page_size != 0) {
         if ((st = check_pages(P)) != FP2_OK) return st;

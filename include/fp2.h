@@ -379,7 +379,8 @@ typedef struct fp2_append_io {
  * q_out may be q itself when q is bf16 rows without a gap; the other buffers
  * must not overlap.  q, k and v are 8-byte aligned, weights and outputs 16.
  * Caches quantised per key block (params->k_block_factor) are not written by
- * this call: FP2_ERR_UNSUPPORTED.  Reads params: heads, head_dim, total_q,
+ * this call, nor are e4m3 ones of head_dim 64, which no call reads:
+ * FP2_ERR_UNSUPPORTED.  Reads params: heads, head_dim, total_q,
  * total_k or page_size and num_pages, scales, workspace, stream. */
 fp2_status fp2_append(const fp2_append_io* io, fp2_dtype dtype, const fp2_params* params);
 
