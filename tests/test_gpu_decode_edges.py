@@ -1,5 +1,5 @@
 """fp2_decode where its arithmetic is at its edges: one key far above a long flat
-tail, scales of 0.  Inputs and bounds as in test_gpu_decode.py."""
+tail, scales of 0, values that are not finite behind a token.  Inputs and bounds as in test_gpu_decode.py."""
 import numpy as np
 import pytest
 import torch
@@ -133,3 +133,53 @@ def test_logits_scales_whose_product_is_zero(n, scale, factor):
     p = c.plan()
     p.run()
     c.check(p)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("Hq,Hkv,d,n,lk", [(8, 2, 128, 4, 130), (2, 2, 128, 16, 24), (8, 1, 128, 3, 1026), (4, 2, 128, 9, 9), (8, 1, 128, 5, 258),
+                                           (8, 1, 64, 4, 130)])
+def test_each_token_sees_its_own_keys_only(dtype, Hq, Hkv, d, n, lk):
+    """Tokens t .. n - 1 overflowed, for every t: the rows below t keep their bits, the others show
+    it, whether it is in their keys or their values."""
+    if dtype == "fp8" and d == 64:
+        pytest.skip("e4m3 is head dimension 128 only")
+    c = Case([n, 1], [lk, 50], Hq, Hkv, d, 16, dtype, seed=46)
+    p = c.plan()
+    p.run()
+    c.check(p)
+    out, lse = p.out.clone(), p.lse.clone()
+    for which in "kv":
+        x = getattr(c, which).view(-1, Hkv, d)
+        raw = x.view(torch.uint8) if dtype == "fp8" else x
+        for bad in ([0x7F] if dtype == "fp8" else [float("nan"), float("inf")]):
+            for t in range(1, n):
+                keep = raw[c.rows[0][lk - n + t:]].clone()
+                raw[c.rows[0][lk - n + t:]] = bad
+                p.run()
+                p.check()
+                assert torch.equal(p.out[:t], out[:t]) and torch.equal(p.lse[:t], lse[:t]), (which, bad, t)
+                assert not torch.isfinite(p.out[t:n].float()).any(), (which, bad, t)
+                assert torch.equal(p.out[n], out[n]) and torch.equal(p.lse[n], lse[n])
+                if which == "v":
+                    assert torch.equal(p.lse[t:n], lse[t:n])
+                else:
+                    assert not torch.isfinite(p.lse[t:n]).any()
+                raw[c.rows[0][lk - n + t:]] = keep
+    p.run()
+    p.check()
+    assert torch.equal(p.out, out) and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("lens,status", [([100, 301, 300], fp2.FP2_ERR_INVALID_ARG), ([100, -1, 300], fp2.FP2_ERR_INVALID_ARG),
+                                         ([100, 0, 300], fp2.FP2_ERR_INVALID_ARG)])
+def test_bad_key_lengths_are_invalid_arguments(n, lens, status):
+    """Above max_seqlen_k, or fewer keys than new tokens: detail 1, and the other sequences stand."""
+    c = Case([n] * 3, [100, 200, 300], 8, 1, 128, 64, seed=47)
+    p = c.plan()
+    c.seqlens_k.copy_(torch.tensor(lens, dtype=torch.int32))
+    p.run()
+    with pytest.raises(fp2.Fp2Error) as e:
+        p.check()
+    assert (e.value.status, e.value.detail) == (status, 1)
+    c.check(p, skip=(1,))
