@@ -183,3 +183,18 @@ def test_bad_key_lengths_are_invalid_arguments(n, lens, status):
         p.check()
     assert (e.value.status, e.value.detail) == (status, 1)
     c.check(p, skip=(1,))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp8", 128), ("bf16", 64)])
+@pytest.mark.parametrize("lk", [[1], [4], [5, 4], [127]])
+@pytest.mark.parametrize("n", [1, 2, 4])
+def test_a_cache_that_ends_with_its_keys(dtype, d, lk, n):
+    """A contiguous cache of fewer rows than one copy takes: what lies behind it is no key."""
+    if min(lk) < n:
+        n = min(lk)
+    c = Case([n] * len(lk), lk, 8, 1, d, 0, dtype, seed=48)
+    rows = sum(lk)
+    c.k, c.v = c.k[:rows], c.v[:rows]
+    p = c.plan()
+    p.run()
+    c.check(p)
