@@ -15,10 +15,11 @@
 // Bound by the rows' bytes.  A lane copies its own 8-byte groups a step ahead into
 // shared memory: no lane waits for another's, 8-byte rows of any stride will do, and
 // no register holds a row on its way.  32768 tokens of 64 + 2 x 8 heads of 128, bf16 to
-// e4m3 (1007 MB): 155 us, 6.48 TB/s; the rows in registers, loaded as they were
-// needed: 178 us; a step ahead in registers: 242 us.  Steps of 4 groups, two of them
-// in shared memory, 6 CTAs on an SM: 155 us; 3 steps of 4: 159; 4 of 4: 196 (the
-// rest of the L1 cache is too small); 4 of 2: 164; 2 of 3: 164; 2 of 6: 165.
+// e4m3 (1007 MB): 156 us, 6.43 TB/s (in a run of seconds at the power limit 180); the rows
+// in registers, loaded as they were needed: 178 us; a step ahead in registers: 242 us.
+// Steps of 4 groups, two of them in shared memory, 6 CTAs on an SM: 155 us when these were
+// compared; 3 steps of 4: 159; 4 of 4: 196 (the rest of the L1 cache is too small); 4 of 2:
+// 164; 2 of 3: 164; 2 of 6: 165.
 // Small calls are bound by their launch (64 tokens: 2.4 us).
 #include <cuda_bf16.h>
 

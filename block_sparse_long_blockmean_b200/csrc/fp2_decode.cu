@@ -21,12 +21,15 @@
 // so that a tile of one token and 8 group heads wastes nothing, and a lane holds the
 // same two rows of S^T and O^T: the softmax's scaling never crosses lanes.
 //
-// Bound by the cache's bytes, each read once.  One sequence of 131072 bf16 keys, 32
-// heads over 8 (537 MB): 87 us, 6.2 TB/s; 128 ragged ones to 8191 keys (2.13 GB): 315
-// us, 6.7 TB/s; 8 e4m3 ones of 4K to 64K (486 MB): 86 us, 5.7 TB/s; 8 ragged bf16
-// ones to 4097 (73 MB): 22 us, of which 4 pass before the first keys are there and 5
-// in the join; one of 1024: 6.8 us, the two launches.  Loads alone reach 6.55 TB/s in
-// pieces of 256 bytes and 5.7 in pieces of 128.
+// Bound by the cache's bytes, each read once for up to 32 packed rows (more are several row
+// tiles, items of their own, each of which reads the keys again: 8 tokens x 8 heads on
+// 131072 e4m3 keys 108 us where 4 tokens take 60).  One sequence of 131072 bf16 keys, 32
+// heads over 8 (537 MB): 87 us, 6.2 TB/s; 128 ragged ones to 8191 keys (2.13 GB): 316 us, 6.7
+// TB/s; 8 e4m3 ones of 4K to 64K (486 MB): 85 us, 5.7 TB/s; 8 ragged bf16 ones to 4097 (73
+// MB): 22 us, of which 4 pass before the first keys are there and 5 in the join; one of 1024:
+// 6.8 us, the two launches; head dimension 64, 131072 keys (268 MB): 54 us, 5.0 TB/s, 128
+// ragged (1.06 GB): 170 us, 6.3 TB/s.  Loads alone reach 6.55 TB/s in pieces of 256 bytes and
+// 5.7 in pieces of 128.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -43,7 +46,8 @@ constexpr int kHeadBytes = 2048;  // of the heads' rows of a token that are read
 
 // Shared memory and shares of a variant: rows of RB bytes, R = 8 NT packed rows.
 // Four warps a CTA, each with a ring of its own: a CTA of 8 warps on each SM leaves it
-// idle at a segment's end (512 sequences of 500 e4m3 keys: 231 us, two of 4 warps 177).
+// idle at a segment's end (512 sequences of 500 e4m3 keys: 231 us where two of 4 warps took
+// 177, before later steps brought them to 101).
 // One tiled copy a unit, head and 128 bytes; a bulk copy per row took 134 us where
 // this takes 95 (128-byte rows: the copies' number counts).
 // A stage of a warp's ring holds the K and V rows of one unit and head, each as
@@ -396,9 +400,11 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
             // with a factor is 0 has made NaN of -inf; the maxima above pass over it)
             if (FP8 && j0 + kUnit > seen_all) mask(w);
             {
-                // weights as the 16-bit operand: fp16 (11 bits) beside e4m3 values;
-                // beside bf16 ones two bf16 terms (16 bits), so that the weights'
-                // rounding stays far below the output's
+                // weights as the 16-bit operand: fp16 (11 bits) beside e4m3 values; beside
+                // bf16 ones two bf16 terms (16 bits).  Either rounding stays far below the
+                // output's: against 64 bits the output is off by 0.0017 of its size with
+                // 32-bit weights and with these.  (A second fp16 term: 512 sequences of 500
+                // e4m3 keys 101 -> 105 us, 2 tokens on 2 x 32768 41 -> 45.)
                 uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -686,16 +692,19 @@ template <int DH, bool FP8, int NT>
 cudaError_t launch(DecodeParams D, cudaStream_t s) {
     using V = Variant<DH, FP8, NT>;
     // more than 16 packed rows at head dimension 128: tiles on the 5th-generation tensor
-    // core (4 tokens x 8 heads on 262144 e4m3 keys: 102 us, here 169); up to 16 rows here
-    // (2 x 8 on 4 x 32768: e4m3 39 us, as tiles 44, bf16 55 and 57)
+    // core (4 tokens x 8 heads on 262144 e4m3 keys: 105 us, in this kernel's form of 32 rows
+    // 169 when it was left).  Up to 16 rows here: 2 tokens x 8 heads, 98 live sequences of 500
+    // keys, bf16 52.9 us, as tiles 57.4, e4m3 45.0 and 55.5; one of 200, 10.2 and 10.9, 10.6
+    // and 12.2; 98 of 2500, 170 and 182, 116 and 118.  One long sequence is the better for
+    // tiles (131072 keys: 93.8 and 86.8, 60.3 and 57.1), but the host does not know the lengths.
     constexpr bool TILES = DH == 128 && NT == 4;
     // (at least one: lengths above a limit of 0 have to be recorded)
     const int packed = D.p.max_seqlen_q > 0 ? D.p.max_seqlen_q * D.p.G : 1;
     // KV heads of an item: those whose rows of a token are 2 KB together, two of them in
     // a CTA where warps take its products, the others in the CTAs beside it, so that
     // the DRAM reads a token's heads at about the same time (128 ragged bf16 sequences:
-    // 319 us, with 1 KB 323, with 512 bytes 332; 4 tokens on 4 x 32768 e4m3 keys: 47,
-    // with 512 bytes 55)
+    // 318 us, with 1 KB 321, with 512 bytes 338; 4 tokens on 2 x 32768 e4m3 keys: 42.6, 42.4
+    // and 45.8)
     D.hw = TILES || D.p.Hkv % 2 ? 1 : 2;
     D.hc = kHeadBytes / V::RB;
     while (D.p.Hkv % D.hc || D.hc % D.hw) --D.hc;
@@ -704,8 +713,8 @@ cudaError_t launch(DecodeParams D, cudaStream_t s) {
     const long long items = (long long)D.p.num_seqs * D.groups * D.tiles_max;
     const int shares = (TILES ? decode_tile_ctas(FP8) : V::CTAS) / (D.hc / D.hw);
     // join by item where an item spans some shares: its parts are shared out over 16 warps
-    // a row (131072 keys: 88.7 us, by share 102.4); else by share, most of 2 or 3 parts
-    // (64 sequences of 1024: 50.4 us, by item 60.4)
+    // a row (131072 keys: 87.8 us, by share 100.0); else by share, most of 2 or 3 parts
+    // (64 sequences of 1024: 48.6 us, by item 55.0)
     D.few = items * 4 <= shares && D.p.num_seqs <= kThreads;
     cudaError_t e;
     if constexpr (TILES) {

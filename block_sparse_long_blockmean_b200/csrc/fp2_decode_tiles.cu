@@ -32,9 +32,12 @@
 //
 // Bound by the cache's bytes and, some 8 us above them, by the softmax's instructions: 4
 // tokens x 8 heads on 262144 e4m3 keys with factors (537 MB) 105 us, 5.1 TB/s (the
-// copies and products alone, with no softmax, 93); 4 x 32768 bf16 keys 54 us.  A run of
-// seconds reaches the power limit and 1.73 GHz: 117 us.  K and V in one ring: 133 us (a
-// value's place stays taken until its product, a key's only until its logits).
+// copies and products alone, with no softmax, 93); on 2 x 32768 bf16 keys (268 MB) 53 us.  A
+// run of seconds reaches the power limit and 1.64 GHz: 120 us.  On short keys a segment's end
+// counts, where the rows pass through shared memory between barriers: 28 live sequences of
+// 2048 e4m3 keys (119 MB) 45 us, of 500 bf16 keys (59 MB) 27.  K and V in one ring, when it was
+// split: 133 us where two took 105 (a value's place stays taken until its product, a key's only
+// until its logits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,8 +58,9 @@ struct Tile {
     static constexpr int HALF = kTileKeys * 128;          // bytes of one
     static constexpr int STAGE = HALVES * HALF;           // a tile of K or of V
     // e4m3 tiles arrive faster than a warpgroup takes their softmax: two CTAs on each
-    // SM (133 us; one, whose rows two warpgroups share, 141).  bf16 stages leave room for
-    // one CTA, and two warpgroups help it (4 x 32768 keys: 58 us, one warpgroup 78).
+    // SM (262144 keys at the time: 133 us; one, whose rows two warpgroups share, 141).  bf16
+    // stages leave room for one CTA, and two warpgroups help it (2 x 32768 keys at the time:
+    // 58 us, one warpgroup 78).
     static constexpr int PER_SM = FP8 ? 2 : 1;
     static constexpr int WGS = FP8 ? 1 : 2;               // softmax warpgroups
     static constexpr int H = kTileRows / WGS;             // rows of one

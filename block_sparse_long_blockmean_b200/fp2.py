@@ -457,7 +457,9 @@ class _Step:
     the error word, and a call whose arguments are marshalled once.  ``run``
     queues it on the stream given at construction, or else on torch's current
     stream of the buffers' device, and returns; ``check`` synchronises that
-    stream and raises on a device-side error."""
+    stream and raises on a device-side error.  A workspace that is given keeps
+    its error word: it is another handle's, or was set up by
+    ``workspace_init``; handles that share one run on one stream."""
 
     def _setup(self, device, stream, workspace, nbytes: int):
         import torch

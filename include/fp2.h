@@ -397,15 +397,19 @@ size_t fp2_decode_workspace_size(const fp2_params* params);
  * The keys of all sequences and KV heads are cut into equal shares, one per
  * CTA, whatever the lengths (they are read on the device, so a captured graph
  * follows them); a head whose keys lie in several shares is joined by a second
- * kernel.  Arguments, supported shapes and dtypes as fp2_attn (block matters
- * for k_block_factor and the page size only); out as fp2_prefill's (an out_scale
- * of 0 stores zeros), rows behind the last sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys
- * may hold anything, NaN included.  out and lse must not overlap the inputs or
- * each other.  group_masks and attn_kernel have no effect.  The workspace's contents need not survive between
- * calls; calls that share one must be ordered on a stream.
+ * kernel.  Logits and sums are fp32.  A weight enters its product with V rounded
+ * to 16 bits (bf16 caches) or 11 (e4m3 ones; fewer for keys whose logit lies more
+ * than 14 below the row's largest, 19 where that one stands far above others, a
+ * block's value factor counting towards it).  Arguments, supported shapes and
+ * dtypes as fp2_attn (block matters for k_block_factor and the page size only);
+ * out as fp2_prefill's (an out_scale of 0 stores zeros), rows behind the last
+ * sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys may hold
+ * anything, NaN included.  out and lse must not overlap the inputs or each other.
+ * group_masks and attn_kernel have no effect.  The workspace's contents need not
+ * survive between calls; calls that share one must be ordered on a stream.
  * max_seqlen_q above FP2_DECODE_MAX_Q: FP2_ERR_UNSUPPORTED (fp2_prefill takes
- * those).  Device-side errors as fp2_attn; a sequence with bad lengths or a
- * page id out of range has undefined out and lse rows, after FP2_ERR_TIMEOUT all
+ * those).  Device-side errors as fp2_attn; a sequence with bad lengths or a page
+ * id out of range has undefined out and lse rows, after FP2_ERR_TIMEOUT all
  * sequences have.  Nothing but the call's own rows is written in either case, and
  * an error that was not read yet does not change the next call's results. */
 fp2_status fp2_decode(const void* q, const void* k_cache, const void* v_cache,
