@@ -338,7 +338,11 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 }
             }
             float2 fac = make_float2(1.f, 1.f);
-            if (FP8 && p.kb_fac) fac = sm_fac[warp][stage];
+            float room = 0.f;
+            if (FP8 && p.kb_fac) {
+                fac = sm_fac[warp][stage];
+                room = room_of(fac.y);
+            }
             auto clear = [&](int from) {  // V rows from..15 of the stage
                 for (int y = max(0, from) * 8 + lane; y < kUnit * 8; y += 32)
 #pragma unroll
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                 w[nt][3] = y.y;
                 top = max3f(max3f(top, x.x, x.y), y.x, y.y);
             }
-            const bool grow = top > kRoof;
+            const bool grow = top > kRoof + room;
             if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -382,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, Variant<DH, FP8, NT>::PER_SM)
                             y = fmaxf(y, __shfl_xor_sync(~0u, y, o));
                             if (FP8) least = fminf(least, __shfl_xor_sync(~0u, least, o));
                         }
-                        if (y + neg_m[nt][e] > kRoof) {
-                            const float lift = lift_of<FP8>(y, least), shrink = ex2(lift - y - neg_m[nt][e]);
+                        if (y + neg_m[nt][e] > kRoof + room) {
+                            const float lift = lift_of<FP8>(y, least) + room, shrink = ex2(lift - y - neg_m[nt][e]);
                             neg_m[nt][e] = lift - y;
                             l[nt][e] *= shrink;
 #pragma unroll

@@ -28,6 +28,10 @@ template <bool FP8>
 __device__ __forceinline__ float lift_of(float most, float least) {
     return FP8 ? fminf(kMostLift, kLift + fmaxf(0.f, most - least - kSpread)) : kLift;
 }
+// What is rounded is the product of the weight and its block's value factor f: it is kept in
+// the range above, by moving the range of the weight (fp32, as are its sums) by 1 / f, so
+// that blocks of small values keep their bits too.  Beyond 2^-60 they lose them.
+__device__ __forceinline__ float room_of(float f) { return fminf(-__log2f(f), 60.f); }
 
 struct DecodeMaps {
     CUtensorMap k, v;  // [rows][Hkv][d], boxes of some rows x 128 bytes of one head

@@ -505,12 +505,13 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                 };
                 auto factor = [&](int i) { return FP8 ? sm_sc[first + i] * fac.x : D.qk_scale; };
                 const uint32_t s_at = tmem + lanes + buf * R + first;
+                const float room = FP8 && p.kb_fac ? room_of(fac.y) : 0.f;
                 float w[H], top = -FLT_MAX;
                 tmem_load(s_at, w);
                 exponents(w);
 #pragma unroll
                 for (int i = 0; i < H; i += 2) top = max3f(top, w[i], w[i + 1]);
-                if (softmax_any(wg, (seen && top > kRoof) || !ok)) {
+                if (softmax_any(wg, (seen && top > kRoof + room) || !ok)) {
                     if (softmax_any(wg, !ok)) {
                         dead = true;
                         break;
@@ -530,9 +531,9 @@ __global__ void __launch_bounds__(Tile<FP8>::THREADS, Tile<FP8>::PER_SM)
                     if (tid < H) {
                         const float most = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
                         const float least = fminf(fminf(red[0][tid], red[1][tid]), fminf(red[2][tid], red[3][tid]));
-                        const float lift = lift_of<FP8>(most, least);
+                        const float lift = lift_of<FP8>(most, least) + room;
                         const float old = sm_nm[first + tid];
-                        const bool moves = most + old > kRoof;
+                        const bool moves = most + old > kRoof + room;
                         sm_f[first + tid] = moves ? ex2(lift - most - old) : 1.f;
                         if (moves) sm_nm[first + tid] = lift - most;
                     }

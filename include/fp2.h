@@ -397,10 +397,10 @@ size_t fp2_decode_workspace_size(const fp2_params* params);
  * The keys of all sequences and KV heads are cut into equal shares, one per
  * CTA, whatever the lengths (they are read on the device, so a captured graph
  * follows them); a head whose keys lie in several shares is joined by a second
- * kernel.  Logits and sums are fp32.  A weight enters its product with V rounded
- * to 16 bits (bf16 caches) or 11 (e4m3 ones; fewer for keys whose logit lies more
- * than 14 below the row's largest, 19 where that one stands far above others, a
- * block's value factor counting towards it).  Arguments, supported shapes and
+ * kernel.  Logits and sums are fp32.  A weight (times its block's value
+ * factor) enters its product with V rounded to 16 bits (bf16 caches) or 11 (e4m3
+ * ones; fewer for keys whose logit lies more than 14 below the row's largest, 19
+ * where that one stands far above others).  Arguments, supported shapes and
  * dtypes as fp2_attn (block matters for k_block_factor and the page size only);
  * out as fp2_prefill's (an out_scale of 0 stores zeros), rows behind the last
  * sequence untouched; lse: fp32 [total_q, Hq] or NULL.  Masked keys may hold

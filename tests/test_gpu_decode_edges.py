@@ -198,3 +198,26 @@ def test_a_cache_that_ends_with_its_keys(dtype, d, lk, n):
     p = c.plan()
     p.run()
     c.check(p)
+
+
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("spread", [0.5, 3.0])
+@pytest.mark.parametrize("factor", [1e-3, 1e-5, 1e-7, 1e-12, "falling", "rising", "mixed"])
+def test_blocks_of_small_values(factor, spread, n):
+    """Value factors far below 1 (one scale for a head whose other sequences, or blocks, hold
+    larger values): what they stand for keeps its precision."""
+    lens = [3000, 40, 9000] if n == 1 else [3000, 40, 700]
+    c = Case([n] * 3, lens, 8, 1, 128, 64, "fp8", seed=49, factors=True, spread=spread)
+    f = c.fac["v"]
+    steps = torch.linspace(0, 1, f.shape[1], device="cuda")[None, :, None]
+    if factor == "falling":
+        f *= 10 ** (-9 * steps)
+    elif factor == "rising":
+        f *= 10 ** (-9 * (1 - steps))
+    elif factor == "mixed":
+        f[:, ::3] *= 1e-4
+    else:
+        f *= factor
+    p = c.plan()
+    p.run()
+    c.check(p)
